@@ -76,8 +76,9 @@ typedef enum hs2_status {
 
 typedef enum hs2_kv_dtype {
   HS2_KV_BF16 = 0,     /* K and V are bfloat16                                      */
-  HS2_KV_FP8_E4M3 = 1  /* K and V are OCP FP8 E4M3 ("fn") codes with per-token
+  HS2_KV_FP8_E4M3 = 1, /* K and V are OCP FP8 E4M3 ("fn") codes with per-token
                           float32 scales: value = decode(code) * scale[b][j]        */
+  HS2_KV_F16 = 2       /* IEEE float16: paged caches and packed prompts only        */
 } hs2_kv_dtype;
 
 /* The shared KV cache of one hybrid block (one K/V head: MQA).
@@ -266,6 +267,148 @@ HS2_API hs2_status hs2_sparse_attn_noalloc(const void* q_layer, int n_q, int h_q
 HS2_API hs2_status hs2_kv_append(const void* k_new, const void* v_new, int n_new,
                                  const hs2_kv* kv, int32_t* lens, void* workspace,
                                  size_t ws_bytes, hs2_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Serving many sequences: a paged cache with grouped K/V heads, and prompts of different
+ * lengths packed together.  The contiguous calls above keep one shared K/V head and one
+ * row range per sequence; a server that admits and retires sequences keeps the cache in
+ * fixed-size pages instead and runs the prompts that arrive together as one call.
+ *
+ *   hs2_packed_attn     causal attention over packed prompts (with or without a prefix)
+ *   hs2_paged_kv_write  new tokens' K/V rows into the pages (quantised when FP8)
+ *   hs2_paged_attn      one new token per sequence over the pages
+ *   hs2_paged_kv_read   rows of the pages back to packed K/V (a prompt's cached prefix)
+ *
+ * The conventions at the top hold, except for the shapes: head_dim is 64 or 128, h_q is
+ * any multiple of n_kv_heads with h_q / n_kv_heads <= 128 (query head h reads K/V head
+ * h / (h_q / n_kv_heads)), and rows have the strides given with them.  All strides are in
+ * elements; those of 8- and 16-bit data are multiples of 16 bytes.
+ * ---------------------------------------------------------------------------------- */
+
+/* A KV cache in pages.  Row r of head h of page p of K (of V) starts at
+ * k + p * page_stride + h * head_stride + r * row_stride (v likewise: the same strides);
+ * its scale is k_scale[p * scale_page_stride + h * scale_head_stride + r * scale_row_stride].
+ * Position j of sequence b is row j % page_size of page pages[b * max_pages + j / page_size].
+ *   k, v       device, head_dim contiguous elements per row: 2 bytes bf16 / float16, or 1
+ *              byte E4M3 code; 16-byte aligned.
+ *   k_scale, v_scale  device float32, one per (token, head), for FP8; NULL otherwise.
+ *              value = decode(code) * scale, with finite scales in [0, 2^60].
+ *   pages      device int32 [batch][max_pages].  Only the entries of positions that a call
+ *              touches are read; a touched entry outside [0, num_pages) sets
+ *              HS2_ERR_INDEX_OUT_OF_RANGE.  Sequences may share pages.
+ *   lens       device int32 [batch]: tokens in the cache, the new ones included.  0 is an
+ *              empty sequence (a padded batch slot); below 0 (taken as 0) or above
+ *              max_pages * page_size (taken as that) sets HS2_ERR_BAD_LENGTH.
+ *   page_size  a power of two in [8, 256].
+ *   max_pages * page_size < 2^31 - 64, batch <= 65535, n_kv_heads <= 1024.             */
+typedef struct hs2_paged_kv {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* pages;
+  const int32_t* lens;
+  int64_t page_stride, head_stride, row_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_row_stride;
+  int32_t batch, max_pages, num_pages, page_size;
+  int32_t n_kv_heads, head_dim;
+  int32_t dtype; /* hs2_kv_dtype */
+} hs2_paged_kv;
+
+/* Bytes of workspace for the three paged calls on this cache with h_q query heads (h_q 0:
+ * hs2_paged_kv_write and hs2_paged_kv_read only); 0 if unsupported.  Zero-filled once
+ * before first use, as the other workspaces; calls that share one must be ordered. */
+HS2_API size_t hs2_paged_workspace_bytes(const hs2_paged_kv* kv, int h_q);
+
+/* Writes new tokens' K and V rows into the pages.  The scheduler that hands out pages
+ * owns the lengths, so unlike hs2_kv_append this call takes lens with the new tokens
+ * already counted and changes nothing but the rows (and scales): token i of the n_b new
+ * tokens of sequence b goes to position lens[b] - n_b + i.
+ *   k_new, v_new  device, type `dtype` (HS2_KV_BF16 or HS2_KV_F16; the cache's own type
+ *             unless it is FP8), row of token t and head h at t * token_stride +
+ *             h * head_stride, 16-byte aligned.
+ *   cu_new    device int32 [batch + 1], ascending from 0: sequence b has the new tokens
+ *             [cu_new[b], cu_new[b + 1]); tokens from cu_new[batch] on are padding and
+ *             ignored.  NULL: n_tokens / batch tokens for every sequence (n_tokens must be
+ *             a multiple of batch).
+ * FP8 rows (one token, one head) get the scale and codes of hs2_kv_append: s = amax / 448
+ * (1 for a zero row), code = row / s, both divisions IEEE float32, saturating.
+ * A sequence with lens[b] < n_b or a bad length is left unwritten (HS2_ERR_BAD_LENGTH), a
+ * row with a bad page too (HS2_ERR_INDEX_OUT_OF_RANGE).  Two tokens for one slot: either's
+ * row, or parts of both.  n_tokens 0 does nothing; n_tokens * n_kv_heads < 2^31. */
+HS2_API hs2_status hs2_paged_kv_write(const void* k_new, const void* v_new, int dtype,
+                                      int64_t token_stride, int64_t head_stride, int n_tokens,
+                                      const int32_t* cu_new, const hs2_paged_kv* kv,
+                                      void* workspace, size_t ws_bytes, hs2_stream_t stream);
+
+/* Reads rows back: packed token i of sequence b (tokens [cu[b], cu[b + 1]), ascending from
+ * 0) is position start[b] + i (start NULL: position i) of the cache, as value =
+ * decode(code) * scale rounded once to `dtype` (HS2_KV_BF16 or HS2_KV_F16; the cache's own
+ * type unless it is FP8).
+ *   k_out, v_out  device, row of token t and head h at t * token_stride + h * head_stride.
+ * Rows from cu[batch] on, rows of positions outside [0, lens[b]) (HS2_ERR_BAD_LENGTH) and
+ * rows of bad pages (HS2_ERR_INDEX_OUT_OF_RANGE) are left as they were.  n_tokens 0 does
+ * nothing; n_tokens * n_kv_heads < 2^31. */
+HS2_API hs2_status hs2_paged_kv_read(const hs2_paged_kv* kv, const int32_t* cu,
+                                     const int32_t* start, int n_tokens, void* k_out,
+                                     void* v_out, int dtype, int64_t token_stride,
+                                     int64_t head_stride, void* workspace, size_t ws_bytes,
+                                     hs2_stream_t stream);
+
+/* Attention of one new token per sequence over its pages: the decode step's full layer for
+ * a paged cache with grouped heads (no selection).
+ *   q        device, type `dtype` (HS2_KV_BF16 or HS2_KV_F16; the cache's own type unless
+ *            it is FP8), head h of sequence b at b * q_seq_stride + h * q_head_stride,
+ *            16-byte aligned.
+ *   sm_scale finite and > 0.
+ *   out      device, type `dtype`, [batch][h_q][head_dim]: softmax(sm_scale q.k) @ V over
+ *            positions [0, lens[b]).
+ *   lse      device float32 [batch][h_q], natural log, or NULL.
+ * An empty sequence gives out 0 and lse -inf.  A bad page's keys count as page 0's (the
+ * sequence's result is then meaningless; no access leaves the cache).  The work is split
+ * over the keys of all sequences and joined in a fixed order: repeated runs on the same
+ * inputs are bitwise identical. */
+HS2_API hs2_status hs2_paged_attn(const void* q, int dtype, int h_q, int64_t q_seq_stride,
+                                  int64_t q_head_stride, const hs2_paged_kv* kv, float sm_scale,
+                                  void* out, float* lse, void* workspace, size_t ws_bytes,
+                                  hs2_stream_t stream);
+
+/* Packed prompts for hs2_packed_attn.  Row of token t and head h of q at
+ * q + t * q_token_stride + h * q_head_stride, of k (of v) at k (v) + t * kv_token_stride +
+ * h * kv_head_stride; 16-byte aligned, head_dim contiguous elements.
+ *   cu_q, cu_k  device int32 [batch + 1], ascending from 0: sequence b has the query tokens
+ *            [cu_q[b], cu_q[b + 1]) and the keys [cu_k[b], cu_k[b + 1]).  cu_k may be cu_q.
+ *   n_q, n_k    rows of q and of k and v (cu_q[batch] <= n_q, cu_k[batch] <= n_k; rows
+ *            behind are padding).
+ *   dtype    HS2_KV_BF16 or HS2_KV_F16, of q, k, v and out. */
+typedef struct hs2_packed {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t q_token_stride, q_head_stride;
+  int64_t kv_token_stride, kv_head_stride;
+  int32_t n_q, n_k, batch, h_q, n_kv_heads, head_dim;
+  int32_t dtype; /* hs2_kv_dtype */
+} hs2_packed;
+
+/* Bytes of workspace for hs2_packed_attn (any sizes), zero-filled once before first use. */
+HS2_API size_t hs2_packed_workspace_bytes(void);
+
+/* Causal attention over packed prompts: query i of the lq of sequence b sits at position
+ * p = lk - lq + i of its lk keys and sees keys [0, p].  lk = lq is a whole prompt; lk > lq a
+ * prompt (or chunk) whose first keys are a cached prefix; with lk < lq the first lq - lk
+ * queries see nothing.
+ *   out      device, type dtype, [n_q][h_q][head_dim]; lse float32 [n_q][h_q], natural log,
+ *            or NULL.  A query that sees nothing gives out 0 and lse -inf.  Rows from
+ *            cu_q[batch] on are left as they were.
+ *   sm_scale finite and > 0.
+ * Non-finite rows of K or V reach only queries of their own sequence, padding rows none.
+ * cu entries that descend or pass n_q / n_k set HS2_ERR_BAD_LENGTH and are clamped.  n_q 0
+ * does nothing; n_q * h_q, n_k * n_kv_heads < 2^31; batch <= 65535. */
+HS2_API hs2_status hs2_packed_attn(const hs2_packed* p, float sm_scale, void* out, float* lse,
+                                   void* workspace, size_t ws_bytes, hs2_stream_t stream);
 
 /* Synchronises `stream` and returns an error the kernels recorded since the last check
  * (HS2_OK if none), then clears them all.  Each kind of error sets its own bit of the

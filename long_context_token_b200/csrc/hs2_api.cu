@@ -10,7 +10,7 @@ namespace hs2 {
 
 static thread_local char g_last_cuda_error[256] = "";
 
-static hs2_status cuda_fail(cudaError_t e, const char* what) {
+hs2_status cuda_fail(cudaError_t e, const char* what) {
   snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", what,
            cudaGetErrorString(e));
   return HS2_ERR_CUDA;

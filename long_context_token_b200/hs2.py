@@ -10,6 +10,16 @@ library).  PyTorch provides device memory and the current stream.
     out, idx, lse = full_attn_select_blocks(q, cache, block=64, workspace=ws)
     out, lse = prefill_attn(q_chunk, cache)          # full layer over a chunk of new tokens
 
+Serving many sequences (grouped K/V heads, a cache in pages, prompts packed together):
+
+    cache = PagedCache(k_pages, v_pages, pages, lens)     # FP8: with k_scale, v_scale
+    ws = paged_workspace(cache, h_q)
+    out, lse = packed_attn(q, k, v, cu_q)                 # causal, prompts of any lengths
+    paged_kv_write(k, v, cache, ws, cu_new=cu_q)          # their rows into the pages
+    paged_kv_write(k_new, v_new, cache, ws)               # one new token per sequence ...
+    out, lse = paged_attn(q_new, cache, ws)               # ... and its attention
+    k, v = paged_kv_read(cache, cu, ws)                   # cached rows back, packed
+
 The library is loaded from ``long_context_token_b200/_lib/libhs2.so``.  There is no
 fallback: if the library is missing or no CUDA device is present, calls raise.
 """
@@ -26,6 +36,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "li
 
 HS2_KV_BF16 = 0
 HS2_KV_FP8_E4M3 = 1
+HS2_KV_F16 = 2
 
 STATUS = {
     0: "HS2_OK", 1: "HS2_ERR_INVALID_ARGUMENT", 2: "HS2_ERR_UNSUPPORTED",
@@ -38,7 +49,9 @@ EXPORTS = ("hs2_workspace_bytes", "hs2_full_attn_select", "hs2_full_attn", "hs2_
            "hs2_last_cuda_error", "hs2_abi_version", "hs2_sparse_attn_noalloc", "hs2_kv_append",
            "hs2_full_attn_select_blocks", "hs2_select_blocks", "hs2_prefill_workspace_bytes",
            "hs2_prefill_attn", "hs2_select_fused", "hs2_workspace_lse64_offset",
-           "hs2_debug_stall_waits", "hs2_set_deterministic")
+           "hs2_debug_stall_waits", "hs2_set_deterministic", "hs2_paged_workspace_bytes",
+           "hs2_paged_kv_write", "hs2_paged_kv_read", "hs2_paged_attn",
+           "hs2_packed_workspace_bytes", "hs2_packed_attn")
 
 
 class Hs2Error(RuntimeError):
@@ -56,6 +69,29 @@ class KV(ctypes.Structure):
                 ("lens", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("max_len", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("scale_row_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class Packed(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("kv_token_stride", ctypes.c_int64), ("kv_head_stride", ctypes.c_int64),
+                ("n_q", ctypes.c_int32), ("n_k", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("h_q", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -115,6 +151,19 @@ def lib():
     L.hs2_debug_stall_waits.restype = None
     L.hs2_set_deterministic.argtypes = [i32]
     L.hs2_set_deterministic.restype = None
+    i64, pgp = ctypes.c_int64, ctypes.POINTER(PagedKV)
+    L.hs2_paged_workspace_bytes.argtypes = [pgp, i32]
+    L.hs2_paged_workspace_bytes.restype = sz
+    L.hs2_paged_kv_write.argtypes = [vp, vp, i32, i64, i64, i32, vp, pgp, vp, sz, vp]
+    L.hs2_paged_kv_write.restype = i32
+    L.hs2_paged_kv_read.argtypes = [pgp, vp, vp, i32, vp, vp, i32, i64, i64, vp, sz, vp]
+    L.hs2_paged_kv_read.restype = i32
+    L.hs2_paged_attn.argtypes = [vp, i32, i32, i64, i64, pgp, f32, vp, vp, vp, sz, vp]
+    L.hs2_paged_attn.restype = i32
+    L.hs2_packed_workspace_bytes.argtypes = []
+    L.hs2_packed_workspace_bytes.restype = sz
+    L.hs2_packed_attn.argtypes = [ctypes.POINTER(Packed), f32, vp, vp, vp, sz, vp]
+    L.hs2_packed_attn.restype = i32
     _lib = L
     return L
 
@@ -386,3 +435,277 @@ def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, cache: Cache, workspace:
 def check_device_status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronise, return (and clear) the first device-side error code (0 = none)."""
     return lib().hs2_check_device_status(workspace.data_ptr(), _stream(stream))
+
+
+# ---------------------------------------------------------------- paged caches, packed prompts
+_FLOAT16S = {torch.bfloat16: HS2_KV_BF16, torch.float16: HS2_KV_F16}
+
+
+def _launch(what: str, device: torch.device, stream, *args) -> None:
+    """Calls a library function on ``device`` (the tensors' own, which need not be the
+    current one) and on ``stream`` (default: that device's current stream)."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(what, device, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device != device:
+        raise ValueError("stream and tensors must be on the same device")
+    _check(getattr(lib(), what)(*args, stream.cuda_stream), what)
+
+
+def _new(stream, make, *shape, **kw) -> torch.Tensor:
+    """A tensor made (torch.empty, torch.zeros) on the stream that uses it."""
+    if stream is None:
+        return make(*shape, **kw)
+    with torch.cuda.stream(stream):
+        return make(*shape, **kw)
+
+
+def _check_on(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, like the other tensors")
+
+
+def _check_int32(name: str, t: torch.Tensor, *shape: int) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
+
+
+def _check_ws(ws: torch.Tensor) -> None:
+    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+
+
+def _row_strides(name: str, t: torch.Tensor) -> Tuple[int, ...]:
+    """Strides of all axes but the last, which must be contiguous.  Axes of one element get
+    the dense stride: theirs is never used and may be anything."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    got, dense = [], t.shape[-1]
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        got.append(s if n > 1 else dense)
+        dense *= n
+    return tuple(reversed(got))
+
+
+class PagedCache:
+    """A KV cache in pages with grouped K/V heads, resident on the device.
+
+    k, v: [num_pages, h_kv, page_size, d] (d 64 or 128, page_size a power of two in
+    [8, 256]), bfloat16, float16, or uint8 / float8_e4m3fn E4M3 codes with k_scale / v_scale
+    float32 [num_pages, h_kv, page_size].  Any strides with a contiguous last axis will do (a
+    cache held as [num_pages, page_size, h_kv, d] is passed as ``cache.transpose(1, 2)``), the
+    same for k and v.  pages int32 [B, max_pages]: the pages of each sequence in order; lens
+    int32 [B]: its length.  Both are read on the device at every call and may change between
+    calls."""
+
+    def __init__(self, k, v, pages, lens, k_scale=None, v_scale=None):
+        if k.dtype == torch.float8_e4m3fn:
+            k, v = k.view(torch.uint8), v.view(torch.uint8)
+        fp8 = k.dtype == torch.uint8
+        if not k.is_cuda:
+            raise ValueError("k must be a CUDA tensor")
+        _check_on(k.device, v=v, pages=pages, lens=lens, k_scale=k_scale, v_scale=v_scale)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [num_pages, h_kv, page_size, d] of one type")
+        if not fp8 and k.dtype not in _FLOAT16S:
+            raise ValueError("k/v must be bfloat16, float16 or E4M3 codes")
+        strides = _row_strides("k", k)
+        if strides != _row_strides("v", v):
+            raise ValueError("k and v must have the same strides")
+        if pages.dim() != 2:
+            raise ValueError("pages must be int32 [B, max_pages]")
+        _check_int32("pages", pages, *pages.shape)
+        _check_int32("lens", lens, pages.shape[0])
+        scale_strides = (0, 0, 0)
+        if fp8:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or t.dtype != torch.float32 or t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be float32 [num_pages, h_kv, page_size]")
+            # (a last axis of one, so that every stride counts as a row's)
+            scale_strides = _row_strides("k_scale", k_scale.unsqueeze(3))
+            if scale_strides != _row_strides("v_scale", v_scale.unsqueeze(3)):
+                raise ValueError("k_scale and v_scale must have the same strides")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("16-bit caches take no scales")
+        self.k, self.v, self.pages, self.lens = k, v, pages, lens
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.dtype = HS2_KV_FP8_E4M3 if fp8 else _FLOAT16S[k.dtype]
+        self._struct = PagedKV(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                               pages.data_ptr(), lens.data_ptr(), *strides, *scale_strides,
+                               pages.shape[0], pages.shape[1], k.shape[0], k.shape[2], k.shape[1],
+                               k.shape[3], self.dtype)
+
+    @property
+    def batch(self) -> int:
+        return self.pages.shape[0]
+
+    @property
+    def h_kv(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3]
+
+    def ref(self):
+        return ctypes.byref(self._struct)
+
+
+def paged_workspace(cache: PagedCache, h_q: int = 0) -> torch.Tensor:
+    """A zero-filled workspace (uint8 tensor) for the paged calls with h_q query heads (0:
+    paged_kv_write and paged_kv_read only)."""
+    n = lib().hs2_paged_workspace_bytes(cache.ref(), h_q)
+    if n == 0:
+        raise Hs2Error(2, "hs2_paged_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def _check_rows(names: Tuple[str, str], k: torch.Tensor, v: torch.Tensor, cache: PagedCache):
+    """Packed rows of a paged cache: their type code and strides."""
+    want = "bfloat16 or float16" if cache.dtype == HS2_KV_FP8_E4M3 else "the cache's type"
+    if k.dim() != 3 or k.shape[1:] != (cache.h_kv, cache.head_dim) or v.shape != k.shape \
+            or v.dtype != k.dtype or k.dtype not in _FLOAT16S \
+            or (cache.dtype != HS2_KV_FP8_E4M3 and _FLOAT16S[k.dtype] != cache.dtype):
+        raise ValueError(f"{names[0]} and {names[1]} must be [T, h_kv, d] of {want}")
+    strides = _row_strides(names[0], k)
+    if strides != _row_strides(names[1], v):
+        raise ValueError(f"{names[0]} and {names[1]} must have the same strides")
+    return _FLOAT16S[k.dtype], strides
+
+
+def paged_kv_write(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedCache,
+                   workspace: torch.Tensor, cu_new: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Writes new tokens' rows [T, h_kv, d] into the pages (quantised, each row with its own
+    scale, when the cache is FP8).  ``cache.lens`` counts them already: token i of the n_b of
+    sequence b goes to position lens[b] - n_b + i.  cu_new int32 [B + 1]: the sequences'
+    ranges of tokens; None: T / B tokens each."""
+    dtype, strides = _check_rows(("k_new", "v_new"), k_new, v_new, cache)
+    _check_on(cache.k.device, k_new=k_new, v_new=v_new, workspace=workspace, cu_new=cu_new)
+    _check_ws(workspace)
+    if cu_new is not None:
+        _check_int32("cu_new", cu_new, cache.batch + 1)
+    _launch("hs2_paged_kv_write", cache.k.device, stream, k_new.data_ptr(), v_new.data_ptr(),
+            dtype, *strides, k_new.shape[0], _ptr(cu_new), cache.ref(), workspace.data_ptr(),
+            workspace.numel())
+
+
+def paged_kv_read(cache: PagedCache, cu: torch.Tensor, workspace: torch.Tensor,
+                  start: Optional[torch.Tensor] = None, n_tokens: Optional[int] = None,
+                  dtype: Optional[torch.dtype] = None, k_out: Optional[torch.Tensor] = None,
+                  v_out: Optional[torch.Tensor] = None, stream=None):
+    """Reads cached rows back (dequantised when FP8): packed token i of sequence b, tokens
+    [cu[b], cu[b + 1]), is position start[b] + i (start None: i).  Returns (k, v), both
+    [n_tokens, h_kv, d]: ``k_out`` and ``v_out``, or new tensors of ``n_tokens`` rows (None:
+    cu[-1], which waits for the device) of ``dtype`` (None: the cache's type, bfloat16 when
+    FP8), zero where no row is read."""
+    _check_int32("cu", cu, cache.batch + 1)
+    if start is not None:
+        _check_int32("start", start, cache.batch)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        if n_tokens is None:
+            n_tokens = int(cu[-1])
+        if dtype is None:
+            dtype = torch.bfloat16 if cache.dtype == HS2_KV_FP8_E4M3 else cache.k.dtype
+        k_out, v_out = (_new(stream, torch.zeros, n_tokens, cache.h_kv, cache.head_dim,
+                             dtype=dtype, device=cache.k.device) for _ in range(2))
+    code, strides = _check_rows(("k_out", "v_out"), k_out, v_out, cache)
+    _check_on(cache.k.device, cu=cu, start=start, k_out=k_out, v_out=v_out, workspace=workspace)
+    _check_ws(workspace)
+    _launch("hs2_paged_kv_read", cache.k.device, stream, cache.ref(), cu.data_ptr(), _ptr(start),
+            k_out.shape[0], k_out.data_ptr(), v_out.data_ptr(), code, *strides,
+            workspace.data_ptr(), workspace.numel())
+    return k_out, v_out
+
+
+def _check_out(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, *shape: int) -> None:
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
+
+
+def paged_attn(q: torch.Tensor, cache: PagedCache, workspace: Optional[torch.Tensor] = None,
+               sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+    """Attention of one new token per sequence over its pages.  q [B, h_q, d] in the cache's
+    type (bfloat16 or float16 when FP8), h_q a multiple of h_kv (query head h reads K/V head
+    h // (h_q // h_kv)), any strides with a contiguous last axis.  Returns (out, lse): out
+    like q and dense, lse float32 [B, h_q]; 0 and -inf for an empty sequence."""
+    if q.dim() != 3 or q.shape[0] != cache.batch or q.shape[2] != cache.head_dim \
+            or q.dtype not in _FLOAT16S \
+            or (cache.dtype != HS2_KV_FP8_E4M3 and _FLOAT16S[q.dtype] != cache.dtype):
+        raise ValueError("queries must be [B, h_q, d] of the cache's type (bfloat16 or float16 "
+                         "for FP8)")
+    B, h_q, d = q.shape
+    strides = _row_strides("q", q)
+    _check_out("out", out, q.dtype, B, h_q, d)
+    _check_out("lse", lse, torch.float32, B, h_q)
+    _check_on(cache.k.device, q=q, out=out, lse=lse, workspace=workspace)
+    if workspace is None:
+        n = lib().hs2_paged_workspace_bytes(cache.ref(), h_q)
+        if n == 0:
+            raise Hs2Error(2, "hs2_paged_workspace_bytes")
+        workspace = _new(stream, torch.zeros, n, dtype=torch.uint8, device=q.device)
+    _check_ws(workspace)
+    if out is None:
+        out = _new(stream, torch.empty, B, h_q, d, dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = _new(stream, torch.empty, B, h_q, dtype=torch.float32, device=q.device)
+    sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
+    _launch("hs2_paged_attn", q.device, stream, q.data_ptr(), _FLOAT16S[q.dtype], h_q, *strides,
+            cache.ref(), sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+            workspace.numel())
+    return out, lse
+
+
+def packed_workspace(device) -> torch.Tensor:
+    """A zero-filled workspace (uint8 tensor) for packed_attn, of any sizes."""
+    return torch.zeros(lib().hs2_packed_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                cu_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                lse: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+    """Causal attention over packed prompts of different lengths.  q [Tq, h_q, d], k and v
+    [Tk, h_kv, d], bfloat16 or float16, d 64 or 128, any strides with a contiguous last axis
+    (the same for k and v; slices of one fused projection will do).  Sequence b has queries
+    [cu_q[b], cu_q[b + 1]) and keys [cu_k[b], cu_k[b + 1]) (cu_k None: cu_q), int32 [B + 1];
+    its last query sees its last key.  Returns (out, lse): out [Tq, h_q, d] like q and dense,
+    lse float32 [Tq, h_q]; 0 and -inf for a query that sees nothing.  Rows behind cu_q[B] are
+    left as they were (zeros, lse -inf, in tensors made here)."""
+    cu_k = cu_q if cu_k is None else cu_k
+    if not q.is_cuda or q.dtype not in _FLOAT16S or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must be bfloat16 or float16 CUDA tensors of one type")
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [Tq, h_q, d], k and v [Tk, h_kv, d]")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must be int32 [B + 1]")
+    B = cu_q.shape[0] - 1
+    _check_int32("cu_q", cu_q, B + 1)
+    _check_int32("cu_k", cu_k, B + 1)
+    tq, h_q, d = q.shape
+    q_strides, kv_strides = _row_strides("q", q), _row_strides("k", k)
+    if kv_strides != _row_strides("v", v):
+        raise ValueError("k and v must have the same strides")
+    _check_out("out", out, q.dtype, tq, h_q, d)
+    _check_out("lse", lse, torch.float32, tq, h_q)
+    _check_on(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, workspace=workspace)
+    if workspace is None:
+        workspace = _new(stream, packed_workspace, q.device)
+    _check_ws(workspace)
+    if out is None:
+        out = _new(stream, torch.zeros, tq, h_q, d, dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = _new(stream, torch.full, (tq, h_q), -math.inf, dtype=torch.float32, device=q.device)
+    sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
+    args = Packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+                  *q_strides, *kv_strides, tq, k.shape[0], B, h_q, k.shape[1], d,
+                  _FLOAT16S[q.dtype])
+    _launch("hs2_packed_attn", q.device, stream, ctypes.byref(args), sm_scale, out.data_ptr(),
+            _ptr(lse), workspace.data_ptr(), workspace.numel())
+    return out, lse

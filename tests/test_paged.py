@@ -1,0 +1,607 @@
+"""Paged caches and packed prompts: every operator against its float64 definition, the
+refusals, and a run of them together.  GPU tests except for the host's checks."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from long_context_token_b200 import build, hs2
+
+from _paged_ref import Pool, TYPES, attend, check, quantise
+
+DEV = "cuda:0"
+
+
+# ---------------------------------------------------------------- the host's checks (CPU)
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return hs2.lib()
+
+
+P = 1 << 20  # an aligned address that no host check dereferences
+
+
+def _kv(**kw):
+    f = dict(k=P, v=P, k_scale=None, v_scale=None, pages=P, lens=P, page_stride=8 * 16 * 128,
+             head_stride=16 * 128, row_stride=128, scale_page_stride=128, scale_head_stride=16,
+             scale_row_stride=1, batch=2, max_pages=4, num_pages=9, page_size=16, n_kv_heads=8,
+             head_dim=128, dtype=0)
+    f.update(kw)
+    return hs2.PagedKV(**f)
+
+
+BAD_CACHES = [
+    (dict(k=None), 1), (dict(pages=None), 1), (dict(lens=None), 1),
+    (dict(k=P + 8), 1),                                # misaligned rows
+    (dict(row_stride=132), 1), (dict(head_stride=-128), 1),  # not whole 16 bytes; negative
+    (dict(row_stride=64), 1),                          # rows overlap
+    (dict(batch=0), 1), (dict(max_pages=0), 1), (dict(num_pages=0), 1), (dict(n_kv_heads=0), 1),
+    (dict(k_scale=P, v_scale=P), 1),                   # a 16-bit cache with scales
+    (dict(dtype=1), 1), (dict(dtype=1, k_scale=P), 1),  # FP8 without its scales
+    (dict(dtype=1, k_scale=P + 2, v_scale=P), 1),
+    (dict(dtype=3), 2), (dict(head_dim=96), 2), (dict(page_size=4), 2), (dict(page_size=24), 2),
+    (dict(page_size=512), 2), (dict(batch=65536), 2), (dict(max_pages=1 << 27), 2),
+]
+
+
+@pytest.mark.parametrize("change,code", BAD_CACHES)
+def test_every_paged_call_refuses_a_bad_cache(L, change, code):
+    kv = ctypes.byref(_kv(**change))
+    big = 1 << 40
+    assert L.hs2_paged_workspace_bytes(kv, 16) == 0
+    assert L.hs2_paged_kv_write(P, P, 0, 1024, 128, 2, P, kv, P, big, None) == code
+    assert L.hs2_paged_kv_read(kv, P, None, 2, P, P, 0, 1024, 128, P, big, None) == code
+    assert L.hs2_paged_attn(P, 0, 16, 2048, 128, kv, 0.1, P, P, P, big, None) == code
+
+
+def test_paged_workspace_sizes(L):
+    kv = ctypes.byref(_kv())
+    assert 4 <= L.hs2_paged_workspace_bytes(kv, 0) <= 512
+    # two partial results of 8 heads x (128 + 2) floats for each of at least 148 CTAs
+    assert L.hs2_paged_workspace_bytes(kv, 64) >= 2 * 148 * 8 * 130 * 4
+    assert L.hs2_paged_workspace_bytes(kv, 12) == 0       # not a multiple of 8 heads
+    assert L.hs2_paged_workspace_bytes(kv, 8 * 129) == 0  # a group above 128
+    assert L.hs2_paged_workspace_bytes(kv, -8) == 0
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(k=None), 1), (dict(k=P + 2), 1), (dict(dtype=2), 1), (dict(dtype=1), 2),
+    (dict(ts=1028), 1), (dict(n=-1), 1), (dict(n=3, cu=None), 1), (dict(ws=None), 1),
+    (dict(ws_bytes=16), 3), (dict(n=(1 << 31) - 1), 2),
+])
+def test_write_and_read_refuse_bad_arguments(L, args, code):
+    a = dict(k=P, dtype=0, ts=1024, n=2, cu=P, ws=P, ws_bytes=1 << 20)
+    a.update(args)
+    kv = ctypes.byref(_kv())
+    assert L.hs2_paged_kv_write(a["k"], P, a["dtype"], a["ts"], 128, a["n"], a["cu"], kv, a["ws"],
+                                a["ws_bytes"], None) == code
+    assert L.hs2_paged_kv_read(kv, a["cu"], None, a["n"], a["k"], P, a["dtype"], a["ts"], 128,
+                               a["ws"], a["ws_bytes"], None) == code
+
+
+def test_nothing_to_move_is_no_error(L):
+    kv = ctypes.byref(_kv())
+    assert L.hs2_paged_kv_write(None, None, 0, 1024, 128, 0, P, kv, P, 4096, None) == 0
+    assert L.hs2_paged_kv_read(kv, P, None, 0, None, None, 0, 1024, 128, P, 4096, None) == 0
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(q=None), 1), (dict(q=P + 8), 1), (dict(out=None), 1), (dict(dtype=2), 1),
+    (dict(dtype=1), 2), (dict(h_q=12), 2), (dict(h_q=0), 2), (dict(qs=2050), 1),
+    (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=math.inf), 1),
+    (dict(scale=math.nan), 1), (dict(lse=P + 2), 1), (dict(ws_bytes=4096), 3),
+])
+def test_paged_attn_refuses_bad_arguments(L, args, code):
+    a = dict(q=P, dtype=0, h_q=16, qs=2048, scale=0.1, out=P, lse=P, ws_bytes=1 << 40)
+    a.update(args)
+    assert L.hs2_paged_attn(a["q"], a["dtype"], a["h_q"], a["qs"], 128, ctypes.byref(_kv()),
+                            a["scale"], a["out"], a["lse"], P, a["ws_bytes"], None) == code
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(cu_q=None), 1), (dict(cu_k=None), 1), (dict(q=None), 1), (dict(k=None), 1),
+    (dict(v=P + 4), 1), (dict(head_dim=32), 2), (dict(dtype=1), 2), (dict(dtype=5), 2),
+    (dict(h_q=7), 2), (dict(h_q=2 * 129), 2), (dict(batch=0), 1), (dict(batch=65536), 2),
+    (dict(n_q=-1), 1), (dict(n_q=1 << 30), 2), (dict(q_token_stride=1025), 1),
+    (dict(kv_head_stride=-128), 1), (dict(scale=math.nan), 1), (dict(ws_bytes=16), 3),
+    (dict(out=P + 8), 1),
+])
+def test_packed_attn_refuses_bad_arguments(L, args, code):
+    f = dict(q=P, k=P, v=P, cu_q=P, cu_k=P, q_token_stride=1024, q_head_stride=128,
+             kv_token_stride=256, kv_head_stride=128, n_q=10, n_k=20, batch=2, h_q=8, n_kv_heads=2,
+             head_dim=128, dtype=0)
+    o = dict(scale=0.1, ws_bytes=1 << 20, out=P)
+    for k, v in args.items():
+        (o if k in o else f)[k] = v
+    p = hs2.Packed(**f)
+    assert L.hs2_packed_attn(ctypes.byref(p), o["scale"], o["out"], P, P, o["ws_bytes"], None) == code
+
+
+def test_no_queries_is_no_error(L):
+    p = hs2.Packed(P, P, P, P, P, 1024, 128, 256, 128, 0, 20, 2, 8, 2, 128, 0)
+    assert L.hs2_packed_attn(ctypes.byref(p), 0.1, None, None, P, 4096, None) == 0
+
+
+# ---------------------------------------------------------------- helpers
+def cu_of(lens):
+    return torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32)
+
+
+def cache_of(pool):
+    return hs2.PagedCache(*pool.to(DEV))
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8 if t.element_size() == 1 else
+                               torch.int16 if t.element_size() == 2 else torch.int32)
+
+
+def same(got, want):
+    return torch.equal(bits(got.cpu()), bits(want))
+
+
+# ---------------------------------------------------------------- writing and reading back
+NEW = [  # lengths after the write, new tokens of each
+    ([1], [1]),
+    ([5, 0, 17, 64, 33, 1], [5, 0, 16, 1, 0, 1]),
+    ([200, 31, 129], [70, 31, 100]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,new", NEW)
+@pytest.mark.parametrize("kv,src", [("bf16", "bf16"), ("f16", "f16"), ("fp8", "bf16"), ("fp8", "f16")])
+@pytest.mark.parametrize("h_kv,d,page,layout", [(1, 128, 16, "hnd"), (3, 64, 8, "nhd"), (8, 128, 64, "nhd"),
+                                                (5, 64, 256, "hnd")])
+def test_write_and_read(lens, new, kv, src, h_kv, d, page, layout):
+    pool = Pool(lens, h_kv, d, page, kv, layout, seed=1, empty=True)
+    g = torch.Generator().manual_seed(2)
+    t = sum(new)
+    pad = 3  # rows behind the last sequence
+    fused = torch.randn(t + pad, 2 * h_kv + 1, d, generator=g)
+    fused[t // 2, 0] = 0  # a zero row: scale 1
+    fused[0, h_kv] *= 1000
+    fused[t:] = math.nan
+    fused = fused.to(TYPES[src]).to(DEV)
+    k_new, v_new = fused[:, :h_kv], fused[:, h_kv:2 * h_kv]  # views of a wider projection
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache)
+    cu = cu_of(new).to(DEV)
+    hs2.paged_kv_write(k_new, v_new, cache, ws, cu_new=cu)
+    assert hs2.check_device_status(ws) == 0
+    at = 0
+    for b, n in enumerate(new):
+        pg, r = pool.at(b, lens[b] - n, lens[b])
+        for x, p, s in ((k_new, pool.k, pool.k_scale), (v_new, pool.v, pool.v_scale)):
+            rows = x[at:at + n].cpu()
+            if kv == "fp8":
+                p[pg, :, r], s[pg, :, r] = quantise(rows)
+            else:
+                p[pg, :, r] = rows
+        at += n
+    want = pool.to("cpu")
+    assert same(cache.k, want[0]) and same(cache.v, want[1])  # the rest untouched, bit for bit
+    if kv == "fp8":
+        assert same(cache.k_scale, want[4]) and same(cache.v_scale, want[5])
+    # read the new rows back from their own start, into tensors with rows behind
+    start = torch.tensor([a - n for a, n in zip(lens, new)], dtype=torch.int32, device=DEV)
+    dt = TYPES[src]
+    k_out, v_out = (torch.full((t + pad, h_kv, d), 7.0, dtype=dt, device=DEV) for _ in range(2))
+    hs2.paged_kv_read(cache, cu, ws, start=start, k_out=k_out, v_out=v_out)
+    assert hs2.check_device_status(ws) == 0
+    assert bool((k_out[t:] == 7).all()) and bool((v_out[t:] == 7).all())
+    wants = [pool.rows(b, lens[b] - n, lens[b]) for b, n in enumerate(new)]
+    for i, got in enumerate((k_out, v_out)):
+        # code * scale is within one float32 rounding of the product; rounding that to 16 bits
+        # lands on the neighbour only where the exact product is at a tie: a step then
+        w = torch.cat([x[i] for x in wants])
+        if kv == "fp8":
+            off = (got[:t].cpu().double() - w).abs()
+            lim = w.abs() * torch.finfo(dt).eps / 2 * (1 + 2.0 ** -10) + torch.finfo(dt).smallest_normal
+            assert bool((off <= lim).all())
+        else:
+            assert same(got[:t], w.to(dt))
+
+
+@pytest.mark.gpu
+def test_uniform_write_is_the_packed_one():
+    lens, n = [40, 9, 1024], 3
+    a, b = (Pool(lens, 2, 128, 32, "fp8", seed=3, empty=True) for _ in range(2))
+    x = torch.randn(2, 9, 2, 128, device=DEV).to(torch.bfloat16)
+    ca, cb = cache_of(a), cache_of(b)
+    ws = hs2.paged_workspace(ca)
+    hs2.paged_kv_write(x[0], x[1], ca, ws)
+    hs2.paged_kv_write(x[0], x[1], cb, ws, cu_new=cu_of([n] * 3).to(DEV))
+    assert same(ca.k, cb.k.cpu()) and same(ca.v_scale, cb.v_scale.cpu())
+    with pytest.raises(hs2.Hs2Error):
+        hs2.paged_kv_write(x[0, :4], x[1, :4], ca, ws)  # 4 tokens for 3 sequences
+
+
+@pytest.mark.gpu
+def test_moves_report_bad_lengths_and_pages_and_touch_nothing():
+    pool = Pool([40, 20, 33], 2, 64, 16, "f16", seed=4)
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache)
+    before = cache.k.clone()
+    x = torch.randn(6, 2, 64, device=DEV).to(torch.float16)
+    cache.lens.copy_(torch.tensor([1, -1, 100], dtype=torch.int32))  # too short; negative; too long
+    hs2.paged_kv_write(x, x, cache, ws)
+    assert hs2.check_device_status(ws) == 7
+    assert same(cache.k, before.cpu())
+    cache.lens.copy_(torch.tensor([40, 20, 33], dtype=torch.int32))
+    good = cache.pages.clone()
+    cache.pages[0, 2], cache.pages[1, 1], cache.pages[2, 2] = -1, pool.num_pages, 1 << 30
+    hs2.paged_kv_write(x, x, cache, ws)
+    assert hs2.check_device_status(ws) == 6
+    k, v = hs2.paged_kv_read(cache, cu_of([40, 20, 33]).to(DEV), ws)
+    assert hs2.check_device_status(ws) == 6
+    assert bool((k[32:40] == 0).all()) and bool((k[40:56] != 0).any())
+    cache.pages.copy_(good)
+    k, v = hs2.paged_kv_read(cache, cu_of([40, 21, 33]).to(DEV), ws)  # one past the second
+    assert hs2.check_device_status(ws) == 7
+    assert bool((k[60] == 0).all()) and bool(torch.isfinite(k).all())
+
+
+# ---------------------------------------------------------------- one new token per sequence
+def run_step(pool, h_q, qtype, strided=False, seed=5, scale=None, **kw):
+    B, d = len(pool.lens), pool.d
+    g = torch.Generator().manual_seed(seed)
+    wide = torch.randn(B, h_q + 3, d, generator=g).to(TYPES[qtype])
+    q = wide[:, 2:2 + h_q] if strided else wide[:, 2:2 + h_q].contiguous()
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache, h_q)
+    qd = wide.to(DEV)[:, 2:2 + h_q] if strided else q.to(DEV)
+    out, lse = hs2.paged_attn(qd, cache, ws, scale, **kw)
+    assert hs2.check_device_status(ws) == 0
+    check_step(pool, q, out, lse, scale)
+    out2, lse2 = hs2.paged_attn(qd, cache, ws, scale)  # the workspace is as it was
+    assert same(out2, out.cpu()) and same(lse2, lse.cpu())
+    return cache, ws, qd, out, lse
+
+
+def check_step(pool, q, out, lse, scale=None):
+    B, h_q, d = q.shape
+    g = h_q // pool.h_kv
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    out, lse = out.cpu(), lse.cpu()
+    # FP8: weights are rounded to float16, whichever type the queries have
+    wt = torch.float16 if pool.kv == "fp8" else q.dtype
+    for b, n in enumerate(pool.lens):
+        k, v = pool.rows(b, 0, n)
+        for h in range(pool.h_kv):
+            hs = slice(h * g, (h + 1) * g)
+            ref = attend(q[b, hs].double(), k[:, h], v[:, h], scale, torch.full((g,), n))
+            check(out[b, hs], lse[b, hs], ref, q.dtype, wt, n, f"sequence {b} ({n}), head {h}")
+
+
+TYPE_PAIRS = [("bf16", "bf16"), ("f16", "f16"), ("fp8", "bf16"), ("fp8", "f16")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,qtype", TYPE_PAIRS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (16, 1), (14, 2), (8, 8), (17, 1), (64, 2), (80, 1), (128, 1)])
+def test_step_heads(kv, qtype, d, h_q, h_kv):
+    run_step(Pool([0, 1, 63, 300, 64, 129], h_kv, d, 16, kv, "nhd", seed=6), h_q, qtype, strided=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,qtype", [("bf16", "bf16"), ("fp8", "bf16")])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256])
+def test_step_pages_and_lengths(kv, qtype, page):
+    """Lengths around the pages' and tiles' edges, table rows wider than any sequence."""
+    lens = [1, page - 1, page, page + 1, 15, 16, 17, 127, 128, 129, 0, 511, 2 * page + 3, 1000]
+    run_step(Pool(lens, 2, 128, page, kv, seed=7, max_pages=1024), 8, qtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,d,h_q,h_kv,lens", [
+    ("bf16", 128, 16, 1, [40000]),          # one sequence over the whole GPU
+    ("fp8", 128, 64, 1, [20011, 3]),
+    ("f16", 64, 4, 4, [9001, 77, 0, 12345]),
+    ("bf16", 128, 8, 2, [300] * 200),       # more sequences than SMs
+    ("fp8", 64, 12, 4, [17, 0, 900, 65, 1] * 30),
+])
+def test_step_split_and_joined(kv, d, h_q, h_kv, lens):
+    run_step(Pool(lens, h_kv, d, 32, kv, seed=8), h_q, "f16" if kv == "f16" else "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_step_large_and_peaked_logits(kv):
+    """Logits of several hundred, rising and falling along the keys, and one key that takes all."""
+    pool = Pool([700, 700, 130], 1, 128, 64, kv, seed=9)
+    ramp = torch.linspace(0, 6, 700)
+    for b, r in ((0, ramp), (1, ramp.flip(0))):
+        pg, row = pool.at(b, 0, 700)
+        if kv == "fp8":
+            pool.k_scale[pg, :, row] *= r[:, None] * 20
+        else:
+            pool.k[pg, :, row] *= r[:, None, None].to(pool.k.dtype)
+    run_step(pool, 16, "bf16", scale=1.0)
+
+
+@pytest.mark.gpu
+def test_step_scales_of_all_sizes():
+    """FP8 rows of V whose scales span 2^-40 .. 2^40 and 0: each weight is held relative to
+    the largest weight times scale."""
+    pool = Pool([513], 2, 128, 16, "fp8", seed=10)
+    pg, row = pool.at(0, 0, 513)
+    for power in (-40, 40):
+        pool.v_scale[pg, :, row] = 2.0 ** power * (1 + torch.rand(513, 2))
+        cache, ws, q, out, lse = None, None, None, None, None
+        g = torch.Generator().manual_seed(11)
+        q = torch.randn(1, 8, 128, generator=g).to(torch.bfloat16)
+        cache = cache_of(pool)
+        ws = hs2.paged_workspace(cache, 8)
+        out, lse = hs2.paged_attn(q.to(DEV), cache, ws)
+        k, v = pool.rows(0, 0, 513)
+        for h in range(2):
+            o, z, a, mag = attend(q[0, 4 * h:4 * h + 4].double(), k[:, h], v[:, h],
+                                  float(torch.tensor(1 / math.sqrt(128.0))), torch.full((4,), 513))
+            f = 2.0 ** -power  # the bound is for values of order 1
+            check(out.cpu()[0, 4 * h:4 * h + 4].double() * f, lse.cpu()[0, 4 * h:4 * h + 4],
+                  (o * f, z, a * f, mag), torch.bfloat16, torch.float16, 513)
+    pool.v_scale[pg, :, row] = 0.0
+    cache = cache_of(pool)
+    out, lse = hs2.paged_attn(q.to(DEV), cache, hs2.paged_workspace(cache, 8))
+    assert bool((out == 0).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.gpu
+def test_step_reports_bad_lengths_and_pages():
+    pool = Pool([100, 60, 33], 2, 128, 16, "bf16", seed=12)
+    for t in (pool.k, pool.v):
+        t.nan_to_num_(0.5)
+    cache, ws, q, out, lse = run_step(pool, 4, "bf16")
+    cache.pages[1, 3] = pool.num_pages
+    out2, lse2 = hs2.paged_attn(q, cache, ws)
+    assert hs2.check_device_status(ws) == 6
+    assert same(out2[0], out[0].cpu()) and same(out2[2], out[2].cpu())  # the others unharmed
+    cache.pages[1, 3] = 0
+    cache.lens[0], cache.lens[2] = -5, 10 ** 9
+    out2, lse2 = hs2.paged_attn(q, cache, ws)
+    assert hs2.check_device_status(ws) in (6, 7)
+    assert bool((out2[0] == 0).all()) and bool((lse2[0] == -math.inf).all())
+
+
+# ---------------------------------------------------------------- packed prompts
+def run_prompts(lq, lk, h_q, h_kv, d, dtype, pad_q=0, pad_k=0, fused=None, scale=None, seed=13):
+    g = torch.Generator().manual_seed(seed)
+    dt = TYPES[dtype]
+    tq, tk = sum(lq), sum(lk)
+    fused = lq == lk if fused is None else fused
+    if fused:
+        x = torch.randn(tq + pad_q, h_q + 2 * h_kv, d, generator=g).to(dt)
+        x[tq:] = math.nan
+        dev = x.to(DEV)
+        cut = (slice(0, h_q), slice(h_q, h_q + h_kv), slice(h_q + h_kv, None))
+        q, k, v = (x[:, c] for c in cut)
+        qd, kd, vd = (dev[:, c] for c in cut)
+    else:
+        q, k, v = (torch.randn(n, h, d, generator=g).to(dt)
+                   for n, h in ((tq + pad_q, h_q), (tk + pad_k, h_kv), (tk + pad_k, h_kv)))
+        q[tq:], k[tk:], v[tk:] = math.nan, math.nan, math.nan
+        qd, kd, vd = q.to(DEV), k.to(DEV), v.to(DEV)
+    cu_q, cu_k = cu_of(lq).to(DEV), cu_of(lk).to(DEV)
+    ws = hs2.packed_workspace(DEV)
+    out = torch.full((tq + pad_q, h_q, d), 7.0, dtype=dt, device=DEV)
+    lse = torch.full((tq + pad_q, h_q), 7.0, device=DEV)
+    hs2.packed_attn(qd, kd, vd, cu_q, cu_k, ws, scale, out=out, lse=lse)
+    assert hs2.check_device_status(ws) == 0
+    assert bool((out[tq:] == 7).all()) and bool((lse[tq:] == 7).all())  # rows behind: left
+    check_prompts(q, k, v, lq, lk, out, lse, scale)
+    out2, lse2 = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    hs2.packed_attn(qd, kd, vd, cu_q, cu_k, ws, scale, out=out2, lse=lse2)
+    assert same(out2, out.cpu()) and same(lse2, lse.cpu())
+
+
+def check_prompts(q, k, v, lq, lk, out, lse, scale=None):
+    d, g = q.shape[2], q.shape[1] // k.shape[1]
+    scale = float(torch.tensor(1.0 / math.sqrt(d) if scale is None else scale, dtype=torch.float32))
+    out, lse = out.cpu(), lse.cpu()
+    a = c = 0
+    for n, m in zip(lq, lk):
+        visible = torch.arange(m - n + 1, m + 1)
+        for h in range(q.shape[1]):
+            ref = attend(q[a:a + n, h].double(), k[c:c + m, h // g].double(), v[c:c + m, h // g].double(),
+                         scale, visible)
+            check(out[a:a + n, h], lse[a:a + n, h], ref, q.dtype, q.dtype, m, f"prompt of {n} on {m}, head {h}")
+        a, c = a + n, c + m
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (4, 4), (8, 2), (7, 1), (6, 2), (16, 1), (80, 1)])
+def test_prompt_heads(dtype, d, h_q, h_kv):
+    run_prompts([1, 130, 0, 37, 64], [1, 130, 0, 37, 64], h_q, h_kv, d, dtype, pad_q=5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[1], [2], [127, 128, 129], [255, 256, 257], [16] * 40, [1] * 70,
+                                  [0, 0, 300, 0], [1025, 3, 700]])
+def test_prompt_lengths(lens):
+    run_prompts(lens, lens, 4, 2, 128, "bf16", pad_q=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("lq,lk", [
+    ([1, 1, 1], [1000, 129, 1]),               # single tokens after long prefixes
+    ([40, 200, 3], [240, 200, 800]),
+    ([50, 0, 20, 9], [20, 30, 0, 9]),          # more queries than keys: the first see nothing
+    ([300], [0]), ([64], [63]),
+])
+def test_prompt_prefixes(d, dtype, lq, lk):
+    run_prompts(lq, lk, 6, 2, d, dtype, pad_q=4, pad_k=9, fused=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_prompt_large_logits(dtype):
+    run_prompts([400, 150], [400, 150], 4, 2, 128, dtype, scale=3.0)
+
+
+@pytest.mark.gpu
+def test_prompt_garbage_stays_in_its_sequence():
+    """Infinities and NaN in one sequence's rows, and in rows no sequence owns, reach no other."""
+    lens = [100, 61, 130]
+    g = torch.Generator().manual_seed(14)
+    q, k, v = (torch.randn(300, h, 64, generator=g).to(torch.bfloat16).to(DEV) for h in (4, 2, 2))
+    cu = cu_of(lens).to(DEV)
+    ws = hs2.packed_workspace(DEV)
+    clean, _ = hs2.packed_attn(q, k, v, cu, workspace=ws)
+    for x in (k, v):
+        x[100:161] = math.nan
+        x[110] = math.inf
+        x[291:] = -math.inf
+    out, _ = hs2.packed_attn(q, k, v, cu, workspace=ws)
+    for rows in (slice(0, 100), slice(161, 291)):
+        assert same(out[rows], clean[rows].cpu())
+
+
+@pytest.mark.gpu
+def test_prompt_reports_bad_offsets():
+    q, k = torch.ones(64, 2, 64, device=DEV).half(), torch.ones(64, 1, 64, device=DEV).half()
+    ws = hs2.packed_workspace(DEV)
+    for cu_q, cu_k in (([0, 30, 65], [0, 30, 64]), ([0, 40, 64], [0, 70, 64]),
+                       ([0, 64, 20], [0, 64, 64]), ([0, 10, 64], [-5, 10, 64])):
+        cu_q, cu_k = (torch.tensor(c, dtype=torch.int32, device=DEV) for c in (cu_q, cu_k))
+        hs2.packed_attn(q, k, k, cu_q, cu_k, ws)
+        assert hs2.check_device_status(ws) == 7
+
+
+# ---------------------------------------------------------------- together, and how they are called
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_served_batch(kv):
+    """Prompts in, their rows into the pages, a second chunk after its cached prefix, then
+    decode steps captured once as a graph and replayed with growing lengths."""
+    h_q, h_kv, d, page = 8, 2, 128, 16
+    first, second, steps = [70, 1, 33], [20, 64, 5], 3
+    total = [a + b + steps for a, b in zip(first, second)]
+    pool = Pool(total, h_kv, d, page, kv, seed=15, empty=True)
+    cache = cache_of(pool)
+    ws, pws = hs2.paged_workspace(cache, h_q), hs2.packed_workspace(DEV)
+    g = torch.Generator().manual_seed(16)
+
+    def proj(n):
+        return torch.randn(n, h_q + 2 * h_kv, d, generator=g).to(torch.bfloat16)
+
+    def cached(b, lo, rows):  # what the cache holds of these rows from position lo on
+        k, v = rows[:, h_q:h_q + h_kv], rows[:, h_q + h_kv:]
+        if kv == "fp8":
+            return tuple((c.view(torch.float8_e4m3fn).double() * s.double()[..., None])
+                         for c, s in (quantise(k), quantise(v)))
+        return k.double(), v.double()
+
+    have = [(torch.zeros(0, h_kv, d).double(),) * 2 for _ in first]
+    lens = [0] * 3
+    for chunk in (first, second):
+        x = proj(sum(chunk))
+        xd = x.to(DEV)
+        q, k, v = xd[:, :h_q], xd[:, h_q:h_q + h_kv], xd[:, h_q + h_kv:]
+        cu = cu_of(chunk).to(DEV)
+        before = list(lens)
+        lens = [a + b for a, b in zip(lens, chunk)]
+        cache.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        hs2.paged_kv_write(k, v, cache, ws, cu_new=cu)
+        cu_k = cu_of(lens).to(DEV)
+        kk, vv = hs2.paged_kv_read(cache, cu_k, ws)  # prefix and chunk, as the cache holds them
+        out, lse = hs2.packed_attn(q, kk, vv, cu, cu_k, pws)
+        at = 0
+        for b, n in enumerate(chunk):
+            new = cached(b, before[b], x[at:at + n])
+            have[b] = tuple(torch.cat([o, w]) for o, w in zip(have[b], new))
+            at += n
+        check_prompts(x[:, :h_q], kk.cpu(), vv.cpu(), chunk, lens, out, lse)
+    # decode
+    xs = [proj(3) for _ in range(steps)]
+    x = xs[0].to(DEV).clone()
+    out = torch.empty(3, h_q, d, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(3, h_q, device=DEV)
+
+    def step():
+        cache.lens.add_(1)
+        hs2.paged_kv_write(x[:, h_q:h_q + h_kv], x[:, h_q + h_kv:], cache, ws)
+        hs2.paged_attn(x[:, :h_q], cache, ws, out=out, lse=lse)
+
+    step()  # warm-up outside the capture; its slot is written again by the first replay
+    cache.lens.sub_(1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(steps):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(3):
+            new = cached(b, lens[b] + i, xs[i][b:b + 1])
+            have[b] = tuple(torch.cat([o, w]) for o, w in zip(have[b], new))
+            for h in range(h_kv):
+                hs = slice(4 * h, 4 * h + 4)
+                n = have[b][0].shape[0]
+                ref = attend(xs[i][b, hs].double(), have[b][0][:, h], have[b][1][:, h],
+                             float(torch.tensor(1 / math.sqrt(128.0))), torch.full((4,), n))
+                check(out.cpu()[b, hs], lse.cpu()[b, hs], ref, torch.bfloat16,
+                      torch.float16 if kv == "fp8" else torch.bfloat16, n, f"step {i}")
+    assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
+
+
+@pytest.mark.gpu
+def test_on_another_stream_and_without_workspaces():
+    pool = Pool([130, 7], 2, 64, 16, "f16", seed=17)
+    cache, ws, q, out, lse = run_step(pool, 6, "f16")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out2, lse2 = hs2.paged_attn(q, cache, stream=s)
+    k, v = hs2.paged_kv_read(cache, cu_of([130, 7]).to(DEV), ws, n_tokens=137, stream=s)
+    torch.cuda.synchronize()
+    assert same(out2, out.cpu()) and same(lse2, lse.cpu())
+    qs = torch.randn(137, 6, 64, device=DEV).half()
+    cu = cu_of([130, 7]).to(DEV)
+    a = hs2.packed_attn(qs, k, v, cu)
+    s.wait_stream(torch.cuda.current_stream())
+    b = hs2.packed_attn(qs, k, v, cu, stream=s)
+    torch.cuda.synchronize()
+    assert same(a[0], b[0].cpu()) and same(a[1], b[1].cpu())
+
+
+@pytest.mark.gpu
+def test_calls_refuse_bad_tensors():
+    pool = Pool([20, 30], 2, 64, 16, "f16", seed=18)
+    k, v, pages, lens, _, _ = pool.to(DEV)
+    cache = hs2.PagedCache(k, v, pages, lens)
+    ws = hs2.paged_workspace(cache, 4)
+    q = torch.zeros(2, 4, 64, device=DEV).half()
+    rows = torch.zeros(2, 2, 64, device=DEV).half()
+    for bad in (lambda: hs2.PagedCache(k.cpu(), v, pages, lens),
+                lambda: hs2.PagedCache(k, v.transpose(1, 2).contiguous().transpose(1, 2), pages, lens),
+                lambda: hs2.PagedCache(k, v, pages.long(), lens),
+                lambda: hs2.PagedCache(k, v, pages, lens[:1]),
+                lambda: hs2.PagedCache(k, v, pages, lens, lens.float(), lens.float()),
+                lambda: hs2.PagedCache(k.float(), v.float(), pages, lens),
+                lambda: hs2.paged_attn(q[:1], cache, ws),
+                lambda: hs2.paged_attn(q.bfloat16(), cache, ws),
+                lambda: hs2.paged_attn(q, cache, ws, out=torch.zeros(2, 4, 64, device=DEV)),
+                lambda: hs2.paged_attn(q, cache, ws.cpu()),
+                lambda: hs2.paged_attn(q, cache, ws.float()),
+                lambda: hs2.paged_kv_write(rows.float(), rows.float(), cache, ws),
+                lambda: hs2.paged_kv_write(rows, rows[:1], cache, ws),
+                lambda: hs2.paged_kv_write(rows, rows, cache, ws, cu_new=lens),
+                lambda: hs2.paged_kv_read(cache, lens, ws),
+                lambda: hs2.packed_attn(q, rows, rows.bfloat16(), lens),
+                lambda: hs2.packed_attn(q, rows, rows, lens[:1]),
+                lambda: hs2.packed_attn(q, rows, rows, lens.cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: hs2.paged_attn(q[:, :3].contiguous(), cache, ws),
+                lambda: hs2.paged_attn(q, cache, ws[:256]),
+                lambda: hs2.paged_attn(q, cache, ws, sm_scale=0.0),
+                lambda: hs2.packed_attn(q[:, :3].contiguous(), rows, rows, lens)):
+        with pytest.raises(hs2.Hs2Error):
+            bad()
