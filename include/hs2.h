@@ -375,7 +375,8 @@ HS2_API hs2_status hs2_paged_attn(const void* q, int dtype, int h_q, int64_t q_s
 
 /* Packed prompts for hs2_packed_attn.  Row of token t and head h of q at
  * q + t * q_token_stride + h * q_head_stride, of k (of v) at k (v) + t * kv_token_stride +
- * h * kv_head_stride; 16-byte aligned, head_dim contiguous elements.
+ * h * kv_head_stride; 16-byte aligned, head_dim contiguous elements.  The stride of an axis
+ * of more than one row is above 0.
  *   cu_q, cu_k  device int32 [batch + 1], ascending from 0: sequence b has the query tokens
  *            [cu_q[b], cu_q[b + 1]) and the keys [cu_k[b], cu_k[b + 1]).  cu_k may be cu_q.
  *   n_q, n_k    rows of q and of k and v (cu_q[batch] <= n_q, cu_k[batch] <= n_k; rows

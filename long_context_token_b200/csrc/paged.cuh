@@ -52,6 +52,10 @@ struct PagedAttnParams {
   float* partials;
 };
 
+// Workspace of hs2_packed_attn: the status word, then at kPackedSyncOff the next work item
+// and the number of CTAs that are done (both 0 between calls).
+constexpr size_t kPackedSyncOff = 256;
+
 struct PackedAttnParams {
   const uint8_t* q;
   const uint8_t* k;
@@ -64,6 +68,7 @@ struct PackedAttnParams {
   void* out;
   float* lse;
   uint32_t* status;
+  uint32_t* sync;
 };
 
 cudaError_t launch_paged_write(const PagedMoveParams& p, int head_dim, int cache_dtype,

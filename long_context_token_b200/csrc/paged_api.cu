@@ -40,6 +40,9 @@ static hs2_status check_paged(const hs2_paged_kv* kv) {
   return HS2_OK;
 }
 
+// A stride that an axis of n elements can be walked with (the tensor maps take no 0).
+static bool walks(int n, int64_t stride) { return n <= 1 || stride > 0; }
+
 static bool check_heads(int h_q, int h_kv) {
   return h_q >= 1 && h_q % h_kv == 0 && h_q / h_kv <= 128;
 }
@@ -195,6 +198,9 @@ hs2_status hs2_packed_attn(const hs2_packed* a, float sm_scale, void* out, float
       !good_stride(a->q_head_stride, 2) || !good_stride(a->kv_token_stride, 2) ||
       !good_stride(a->kv_head_stride, 2) || ((uintptr_t)lse & 3u))
     return HS2_ERR_INVALID_ARGUMENT;
+  if (!walks(a->n_q, a->q_token_stride) || !walks(a->h_q, a->q_head_stride) ||
+      !walks(a->n_k, a->kv_token_stride) || !walks(a->n_kv_heads, a->kv_head_stride))
+    return HS2_ERR_INVALID_ARGUMENT;
   if (!workspace || !aligned16(workspace)) return HS2_ERR_INVALID_ARGUMENT;
   if (ws_bytes < hs2_packed_workspace_bytes()) return HS2_ERR_WORKSPACE_TOO_SMALL;
   if (a->n_q == 0) return HS2_OK;
@@ -221,6 +227,7 @@ hs2_status hs2_packed_attn(const hs2_packed* a, float sm_scale, void* out, float
   p.out = out;
   p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
+  p.sync = ws_ptr<uint32_t>(workspace, kPackedSyncOff);
   const cudaError_t e = launch_packed_attn(p, a->head_dim, a->dtype, stream);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e, "packed attention launch");
 }

@@ -298,6 +298,11 @@ bool make_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint
                   uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                   CUtensorMapSwizzle swizzle);
 
+// Host: tiled tensor map of 2 to 5 axes, innermost first (strides of axes 1 .. rank - 1).
+bool make_tmap_nd(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank,
+                  const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                  CUtensorMapSwizzle swizzle);
+
 cudaError_t launch_full_attn_tc(const FullParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 int bq, cudaStream_t st);
 // Sparse layer through the same kernel in gather mode (p.idx, p.idx_width, p.out set):
