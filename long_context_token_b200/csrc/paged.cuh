@@ -14,6 +14,10 @@ namespace hs2 {
 // head), then the partial results of the CTAs (two per CTA of paged_attn).
 constexpr size_t kPagedCounterOff = 256;
 constexpr int kPagedMaxCtas = kSmCountBound;
+// Floats of one partial result: o [group][head_dim], then (m, l) of each head.
+__host__ __device__ constexpr int paged_part_floats(int group, int head_dim) {
+  return (group * (head_dim + 2) + 3) / 4 * 4;
+}
 
 struct PagedView {
   uint8_t* k;

@@ -15,6 +15,9 @@ static bool good_stride(int64_t elements, int elt) {
   return elements >= 0 && elements < (int64_t(1) << 38) && elements * elt % 16 == 0;
 }
 
+// A stride that an axis of n elements can be walked with (the tensor maps take no 0).
+static bool walks(int n, int64_t stride) { return n <= 1 || stride > 0; }
+
 static hs2_status check_paged(const hs2_paged_kv* kv) {
   if (!kv || !kv->k || !kv->v || !kv->pages || !kv->lens) return HS2_ERR_INVALID_ARGUMENT;
   if (kv->head_dim != 64 && kv->head_dim != 128) return HS2_ERR_UNSUPPORTED;
@@ -32,16 +35,14 @@ static hs2_status check_paged(const hs2_paged_kv* kv) {
   const int elt = fp8 ? 1 : 2;
   if (!aligned16(kv->k) || !aligned16(kv->v) || !good_stride(kv->page_stride, elt) ||
       !good_stride(kv->head_stride, elt) || !good_stride(kv->row_stride, elt) ||
-      kv->row_stride < kv->head_dim)
+      kv->row_stride < kv->head_dim || !walks(kv->num_pages, kv->page_stride) ||
+      !walks(kv->n_kv_heads, kv->head_stride))
     return HS2_ERR_INVALID_ARGUMENT;
   if (fp8 && (((uintptr_t)kv->k_scale | (uintptr_t)kv->v_scale) & 3u || kv->scale_page_stride < 0 ||
               kv->scale_head_stride < 0 || kv->scale_row_stride < 0))
     return HS2_ERR_INVALID_ARGUMENT;
   return HS2_OK;
 }
-
-// A stride that an axis of n elements can be walked with (the tensor maps take no 0).
-static bool walks(int n, int64_t stride) { return n <= 1 || stride > 0; }
 
 static bool check_heads(int h_q, int h_kv) {
   return h_q >= 1 && h_q % h_kv == 0 && h_q / h_kv <= 128;
@@ -53,7 +54,7 @@ static size_t paged_bytes(const hs2_paged_kv* kv, int h_q) {
   size_t n = kPagedCounterOff;
   if (h_q) {
     n += ((size_t)kv->batch * kv->n_kv_heads * 4 + 255) / 256 * 256;
-    n += (size_t)2 * kPagedMaxCtas * (h_q / kv->n_kv_heads) * (kv->head_dim + 2) * 4;
+    n += (size_t)2 * kPagedMaxCtas * paged_part_floats(h_q / kv->n_kv_heads, kv->head_dim) * 4;
   }
   return n;
 }

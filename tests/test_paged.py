@@ -300,6 +300,10 @@ def test_step_pages_and_lengths(kv, qtype, page):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv,d,h_q,h_kv,lens", [
     ("bf16", 128, 16, 1, [40000]),          # one sequence over the whole GPU
+    ("bf16", 128, 16, 1, [131072] * 2),     # dozens of tiles for each CTA: the ring goes round
+    ("f16", 128, 3, 1, [90001, 1, 100000]),
+    ("fp8", 64, 16, 1, [200000, 131]),
+    ("fp8", 128, 20, 1, [150000]),
     ("fp8", 128, 64, 1, [20011, 3]),
     ("f16", 64, 4, 4, [9001, 77, 0, 12345]),
     ("bf16", 128, 8, 2, [300] * 200),       # more sequences than SMs
