@@ -2,22 +2,26 @@
 //
 // Per key and K/V head the kernel reads two rows (K and V) and spends 4 D flop on each of
 // the group's queries, so memory bounds it up to groups of about 64; the work is laid out
-// to stream pages without a pause.  The 64-key tiles of all (sequence, K/V head) pairs form
+// to stream pages without a pause.  The 32-key tiles of all (sequence, K/V head) pairs form
 // one line, cut into equal runs, one per persistent CTA (one CTA per SM), so ragged batches
 // and single long sequences both fill the GPU.
 //
-//   producer warp  page table look-ups (a window of 32 entries ahead) and one TMA load per
-//                  page and tensor into a ring of tiles (160 KB in flight per SM); float32
-//                  scales of an FP8 cache by 4-byte asynchronous copies.
-//   8 warps        flash decoding with mma.sync m16n8k16: 16 query heads of the group are
-//                  the rows, 16 keys a step.  The tensor work is a few per cent of the
-//                  time, and fragments in registers need no TMEM round trip per 64 keys,
-//                  so tcgen05 would only lengthen each tile's chain.  The warps split the
-//                  head tiles first, then the keys; each keeps its own reference, sums and
-//                  outputs, joined through shared memory when a (sequence, head) pair ends.
+//   4 producer warps  take the run's tiles in turn: page table look-ups (a window of 32
+//                  entries ahead), one TMA load per page and tensor into a ring of 128 KB,
+//                  float32 scales of an FP8 cache by 4-byte asynchronous copies.  (One warp
+//                  spends about 600 cycles on a tile, 1200 with scales: too slow alone.)
+//   8 warps        flash decoding with mma.sync m16n8k16, transposed: S^T = K Q^T with 16
+//                  keys as the rows and 8 heads as the columns, O^T += V^T P^T, so a group
+//                  of 7 or 8 heads wastes nothing and P goes from accumulator to operand
+//                  by a transposing move within the warp.  The tensor work is a few per
+//                  cent of the time, and fragments in registers need no TMEM round trip per
+//                  tile, so tcgen05 would only lengthen each tile's chain.  A warp takes a
+//                  whole tile for 8 or 16 heads; warps with the same heads take tiles in
+//                  turn and keep their own references, sums and outputs, joined through
+//                  shared memory when a (sequence, head) pair ends.
 //
 // The softmax reference moves only when a logit passes it by more than 8 (log2 units), so a
-// step has no shuffles.  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
+// tile has no shuffles.  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
 // with m following max(x + log2 s_v), so w <= 2^8 is rounded to float16 relative to the
 // largest weight however the scales vary; E4M3 codes are exact in float16.  A bfloat16
 // query against codes is brought to float16 by a power of two per head, exactly down to
@@ -35,30 +39,37 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kTileKeys = 64;
+constexpr int kTileKeys = 32;
 constexpr int kConsumers = 256;
-constexpr int kPagedThreads = kConsumers + 32;
-constexpr int kMinTiles = 2;  // a run is at least this many tiles
+constexpr int kProducerWarps = 4;
+constexpr int kPagedThreads = kConsumers + 32 * kProducerWarps;
+// Joining one partial result of one element costs this much of a tile's time in a run
+// (measured on a B200: about 65 ns per 16 heads x 128, against 0.25 us per tile of a run).
+constexpr float kJoinCost = 0.25f / 2048.f;
+constexpr int kMinTiles = 8;  // a run is at least a tile for each warp
 constexpr float kMoveAt = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int D, bool kFp8>
+// NT: 8-head tiles per warp.
+template <int D, bool kFp8, int NT>
 struct PagedSmem {
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
   static constexpr int kTile = kTileKeys * kRowBytes;  // K or V
   static constexpr int kScales = kFp8 ? 2 * kTileKeys * 4 : 0;
-  static constexpr int kFit = 160 * 1024 / (2 * kTile + kScales);
-  // Even: where two groups of warps take alternate tiles, each stage then always belongs to
-  // the same group, which so waits for every phase of its barrier.  (A parity wait that skips
-  // a phase passes too early when the skipped phase's data is late.)
-  static constexpr int kStages = kFit > 16 ? 16 : kFit / 2 * 2;
+  // 128 KB of rows.  A multiple of 8 (and of the producer warps): warps that take tiles in
+  // turn then always find theirs in the same stages, so they wait for every phase of those
+  // stages' barriers.  (A parity wait that skips a phase passes too early when the skipped
+  // phase's data is late.)
+  static constexpr int kStages = 128 * 1024 / (2 * kTile);
   static constexpr uint32_t kScaleOff = kStages * 2 * kTile;
   static constexpr uint32_t kRedOff = kScaleOff + kStages * kScales;
-  static constexpr uint32_t kMlOff = kRedOff + 8 * 16 * D * 4;  // [8 warps][16][2]
-  static constexpr uint32_t kBarOff = kMlOff + 8 * 16 * 8;
+  static constexpr uint32_t kRedFloats = 8 * 8 * NT * D;  // [8 warps][8 NT heads][D]
+  static constexpr uint32_t kMlOff = kRedOff + kRedFloats * 4;  // [8 warps][8 NT heads] (m, l)
+  static constexpr uint32_t kBarOff = kMlOff + 8 * 8 * NT * 8;
   static constexpr uint32_t kMiscOff = kBarOff + 2 * kStages * 8;
-  static constexpr uint32_t kBytes = kMiscOff + 128 + 1024;
-  static_assert(kBytes <= 227 * 1024 && kStages % 2 == 0, "shared memory budget");
+  static constexpr uint32_t kBytes = kMiscOff + 64 + 1024;
+  static_assert(kBytes <= 227 * 1024 && kStages % 8 == 0 && kStages % kProducerWarps == 0,
+                "shared memory budget");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -99,28 +110,28 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// One run of the tile line: where a CTA starts and how far it goes.
-struct Run {
-  long long total, per, begin, end;  // tiles
-  int b;                             // sequence of tile `begin`
-  long long b_first;                 // the line's tile at which that sequence starts
-};
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
 // A (sequence, K/V head) pair's part of the run, the same walk for all warps.
 struct Segment {
   int b, h, len, t0, nt, tiles;  // tiles [t0, t0 + nt) of the pair's `tiles`
-  long long first;               // the line's tile at which the pair starts
+  int first;                     // the line's tile at which the pair starts
 };
 
 struct Walk {
-  long long at, end, b_first;
-  int b;
+  int at, end;   // the rest of the run, in the line's tiles
+  int b;         // sequence
+  int b_first;   // the line's tile at which it starts
   __device__ bool next(const PagedAttnParams& p, Segment& s) {
     if (at >= end) return false;
     int len = paged_len(p.c, b, false);
     int tiles = (len + kTileKeys - 1) / kTileKeys;
-    while (at >= b_first + (long long)tiles * p.c.h_kv) {  // (also over empty sequences)
-      b_first += (long long)tiles * p.c.h_kv;
+    while (at >= b_first + tiles * p.c.h_kv) {  // (also over empty sequences)
+      b_first += tiles * p.c.h_kv;
       ++b;
       len = paged_len(p.c, b, false);
       tiles = (len + kTileKeys - 1) / kTileKeys;
@@ -128,11 +139,11 @@ struct Walk {
     s.b = b;
     s.len = len;
     s.tiles = tiles;
-    const long long in = at - b_first;
-    s.h = (int)(in / tiles);
-    s.t0 = (int)(in - (long long)s.h * tiles);
-    s.first = b_first + (long long)s.h * tiles;
-    s.nt = (int)min((long long)(tiles - s.t0), end - at);
+    const int in = at - b_first;
+    s.h = in / tiles;
+    s.t0 = in - s.h * tiles;
+    s.first = at - s.t0;
+    s.nt = min(tiles - s.t0, end - at);
     at += s.nt;
     return true;
   }
@@ -140,31 +151,32 @@ struct Walk {
 
 }  // namespace
 
-template <int D, typename Q, bool kFp8>
+template <int D, typename Q, bool kFp8, int NT>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, PagedAttnParams p) {
-  using L = PagedSmem<D, kFp8>;
+  using L = PagedSmem<D, kFp8, NT>;
   constexpr int NS = L::kStages;
   constexpr int RB = L::kRowBytes;
   constexpr bool kBf16 = !kFp8 && !std::is_same<Q, __half>::value;  // the MMAs' type
   constexpr bool kScaleQ = kFp8 && !std::is_same<Q, __half>::value;
   constexpr int KS = D / 16;  // MMA steps along D
+  constexpr int HT = 8 * NT;  // heads of a warp
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   float* red = reinterpret_cast<float*>(smem + L::kRedOff);
   float2* red_ml = reinterpret_cast<float2*>(smem + L::kMlOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + NS;
-  long long* misc = reinterpret_cast<long long*>(smem + L::kMiscOff);  // [0..3] the run, [4..] scan
-  int* flag = reinterpret_cast<int*>(smem + L::kMiscOff + 120);
+  int* misc = reinterpret_cast<int*>(smem + L::kMiscOff);  // 0..3 the run, 4..11 scan, 12 flag
 
   const int warp = threadIdx.x >> 5, lane = (int)lane_id();
-  const int mt = p.group <= 16 ? 1 : p.group <= 32 ? 2 : p.group <= 64 ? 4 : 8;  // head tiles
+  // Warps that share the heads of a tile of the group, and warps per key tile.
+  const int mt = NT == 1 || p.group <= 16 ? 1 : p.group <= 32 ? 2 : p.group <= 64 ? 4 : 8;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full + s, kFp8 ? 33 : 1);
-      mbar_init(empty + s, mt == 1 ? 4 : 8);
+      mbar_init(empty + s, mt);
     }
     fence_mbar_init();
   }
@@ -174,44 +186,50 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   }
   griddep_wait();
 
-  // ---- the run: a prefix sum of the sequences' tiles, kConsumers threads of `each` sequences
+  // ---- the run: a prefix sum of the sequences' tiles, 256 threads of `each` sequences
   {
-    long long* sums = misc + 4;  // [8]
-    const int each = (p.c.batch + kConsumers - 1) / kConsumers;
-    long long mine = 0;
+    const int each = (p.c.batch + 255) / 256;
+    int mine = 0, longest = 0;
     const int b_lo = min((int)threadIdx.x * each, p.c.batch), b_hi = min(b_lo + each, p.c.batch);
     if (warp < 8)
-      for (int b = b_lo; b < b_hi; ++b)
-        mine += (paged_len(p.c, b, blockIdx.x == 0) + kTileKeys - 1) / kTileKeys;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const int n = (paged_len(p.c, b, blockIdx.x == 0) + kTileKeys - 1) / kTileKeys;
+        mine += n;
+        longest = max(longest, n);
+      }
     mine *= p.c.h_kv;
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (warp < 8 && lane == 31) sums[warp] = incl;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (warp < 8 && lane == 31) misc[4 + warp] = incl;
+    if (threadIdx.x == 0) misc[2] = misc[3] = 0;
+    // (the warps' longest sequences meet in the not yet used result buffer)
+    if (warp < 8 && lane == 0) reinterpret_cast<int*>(red)[warp] = longest;
     __syncthreads();
-    long long before = incl - mine, total = 0;
+    int before = incl - mine, total = 0;
     for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+      if (w < warp) before += misc[4 + w];
+      total += misc[4 + w];
+      longest = max(longest, reinterpret_cast<int*>(red)[w]);
     }
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinTiles) per = kMinTiles;
-    const long long begin = (long long)blockIdx.x * per;
+    // Equal runs; but a pair cut into n runs costs the last of them n partial results to
+    // join, so short lines are cut less: about as long a run as joining its pair takes.
+    int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int cut = (int)sqrtf((float)longest * (float)(p.group * D) * kJoinCost);
+    per = max(max(per, cut), kMinTiles);
+    const int begin = (int)min((long long)blockIdx.x * per, (long long)total);
     if (threadIdx.x == 0) {
       misc[0] = per;
-      misc[1] = min(begin + per, total);
-      misc[2] = 0;
-      misc[3] = 0;
+      misc[1] = (int)min((long long)begin + per, (long long)total);
     }
-    __syncthreads();
     if (warp < 8 && begin >= before && begin < before + mine) {
       int b = b_lo;
       for (;; ++b) {
-        const long long n =
-            (long long)((paged_len(p.c, b, false) + kTileKeys - 1) / kTileKeys) * p.c.h_kv;
+        const int n = (paged_len(p.c, b, false) + kTileKeys - 1) / kTileKeys * p.c.h_kv;
         if (begin < before + n) break;
         before += n;
       }
@@ -220,11 +238,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     }
     __syncthreads();
   }
-  const long long per = misc[0];
+  const int per = misc[0];
   Walk walk;
-  walk.at = (long long)blockIdx.x * per;
   walk.end = misc[1];
-  walk.b = (int)misc[2];
+  walk.at = (int)min((long long)blockIdx.x * per, (long long)walk.end);
+  walk.b = misc[2];
   walk.b_first = misc[3];
   bool ok = true;
   // A wait that gives up is recorded; the loops then run to their end without waiting (every
@@ -237,12 +255,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   };
   Segment s;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer
-    const int shift = p.c.page_shift;
+  if (warp >= 8) {
+    // ------------------------------------------------------------ producers
+    const int me = warp - 8;
+    const int shift = p.c.page_shift, in_page = (1 << shift) - 1;
     const int rows = min(1 << shift, kTileKeys);  // rows of one load
     const uint32_t box_bytes = (uint32_t)rows * RB;
-    uint32_t slot = 0;
+    uint32_t slot = 0;  // this run's tiles so far
+    uint32_t mine = 0;  // of them, this warp's last one + 1 (0: none)
     while (ok && walk.next(p, s)) {
       const int32_t* table = p.c.pages + (size_t)s.b * p.c.max_pages;
       const int last_page = (s.len - 1) >> shift;
@@ -257,12 +277,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         return id;
       };
+      // (a tile's pages never straddle two windows: both start at whole tiles)
       int base = (s.t0 * kTileKeys) >> shift;
       int ids = load_pages(base), ids_next = load_pages(base + 32);
       for (int t = s.t0; t < s.t0 + s.nt; ++t, ++slot) {
+        if ((int)(slot % kProducerWarps) != me) continue;
         const int key0 = t * kTileKeys, keys = min(s.len - key0, kTileKeys);
-        const int n = (keys + rows - 1) / rows;  // loads per tensor, at most 8
-        if (((key0 + (n - 1) * rows) >> shift) >= base + 32) {
+        const int n = (keys + rows - 1) / rows;  // loads per tensor, at most 4
+        while (((key0 + (n - 1) * rows) >> shift) >= base + 32) {
           base += 32;
           ids = ids_next;
           ids_next = load_pages(base + 32);
@@ -278,27 +300,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         if (i < n) {
           const uint32_t dst = smem_u32(smem + st * 2 * L::kTile) + (lane < 16 ? 0 : L::kTile) +
                                i * box_bytes;
-          tma_load_5d(dst, lane < 16 ? &tmap_k : &tmap_v, full + st, 0, key & ((1 << shift) - 1), 0,
-                      s.h, id);
+          tma_load_5d(dst, lane < 16 ? &tmap_k : &tmap_v, full + st, 0, key & in_page, 0, s.h, id);
         }
         if constexpr (kFp8) {
-          const uint32_t dst = smem_u32(smem + L::kScaleOff + st * L::kScales);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int r = lane + 32 * u, k = key0 + min(r, keys - 1);
-            const int pg = __shfl_sync(0xffffffffu, ids, (k >> shift) - base);
-            if (r < keys) {
-              const int64_t at = pg * p.c.sc_page + s.h * p.c.sc_head + (k & ((1 << shift) - 1)) * p.c.sc_row;
-              cp_async_4(dst + r * 4, p.c.k_scale + at);
-              cp_async_4(dst + (kTileKeys + r) * 4, p.c.v_scale + at);
-            }
+          const uint32_t dst = smem_u32(smem + L::kScaleOff + st * L::kScales) + lane * 4;
+          const int k = key0 + min(lane, keys - 1);
+          const int pg = __shfl_sync(0xffffffffu, ids, (k >> shift) - base);
+          if (lane < keys) {
+            const int64_t at = pg * p.c.sc_page + s.h * p.c.sc_head + (k & in_page) * p.c.sc_row;
+            cp_async_4(dst, p.c.k_scale + at);
+            cp_async_4(dst + kTileKeys * 4, p.c.v_scale + at);
           }
           cp_async_arrive(full + st);
         }
+        mine = slot + 1;
       }
     }
-    // No load may outlive the CTA.
-    for (uint32_t x = slot > NS ? slot - NS : 0; x < slot; ++x) mbar_wait(full + x % NS, (x / NS) & 1);
+    // No load may outlive the CTA: this warp's last fill of each of its stages.
+    for (uint32_t x = mine; x > 0 && mine - x < NS; x -= min(x, (uint32_t)kProducerWarps))
+      mbar_wait(full + (x - 1) % NS, ((x - 1) / NS) & 1);
   } else {
     // ------------------------------------------------------------ consumers
     // Empty sequences have no tiles: their rows are written here, spread over the CTAs.
@@ -309,10 +329,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       if (p.lse)
         for (int e = threadIdx.x; e < p.h_q; e += kConsumers) p.lse[(size_t)b * p.h_q + e] = -INFINITY;
     }
-    const int m_tile = warp % mt, slice = warp / mt, slices = 8 / mt;
-    const int blocks = mt <= 2 ? 1 : mt / 2;  // 16-key steps of a tile per warp
-    const int c4 = lane & 3, r0 = lane >> 2;
-    const int rshift = min(p.c.page_shift, 6);  // rows of one load, log2
+    const int m_tile = warp % mt, turn = warp / mt, turns = 8 / mt;
+    const int c4 = lane & 3, r8 = lane >> 2;
+    const int rshift = min(p.c.page_shift, 5);  // rows of one load, log2
     // Byte offset within a tile of 16-byte chunk `c` of key `r`, in the layout TMA wrote.
     auto at = [&](int r, int c) -> uint32_t {
       if constexpr (RB == 256)
@@ -325,262 +344,269 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     };
     uint32_t slot = 0;
     while (walk.next(p, s)) {
-      // ---- queries: rows r0 and r0 + 8 of this warp's head tile
-      uint32_t qa[KS][4];
-      float f0 = 1.f, f1 = 1.f;  // 1 / the power of two that a query row was multiplied by
-      {
-        const int h0 = m_tile * 16 + r0;
-        const uint8_t* q0 = p.q + (int64_t)s.b * p.q_seq + (int64_t)(s.h * p.group + h0) * p.q_head;
-        const uint8_t* q1 = q0 + 8 * p.q_head;
-        const bool v0 = h0 < p.group, v1 = h0 + 8 < p.group;
+      // ---- queries, as the MMA's K x N operand: head r8 of each 8-head tile
+      uint32_t qb[KS][NT][2];
+      float f[NT][2];  // factors of the logits of heads 2 c4 and 2 c4 + 1
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int h = m_tile * HT + n * 8 + r8;
+        const uint8_t* q = p.q + (int64_t)s.b * p.q_seq + (int64_t)(s.h * p.group + h) * p.q_head;
+        const bool have = h < p.group;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           // FP8: a step's 16 elements in the order of the codes' registers (4 per thread)
           const int e0 = 16 * k + (kFp8 ? 4 * c4 : 2 * c4), e1 = kFp8 ? e0 + 2 : e0 + 8;
-          qa[k][0] = v0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 2 * e0)) : 0u;
-          qa[k][1] = v1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + 2 * e0)) : 0u;
-          qa[k][2] = v0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + 2 * e1)) : 0u;
-          qa[k][3] = v1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + 2 * e1)) : 0u;
+          qb[k][n][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e0)) : 0u;
+          qb[k][n][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e1)) : 0u;
         }
+        float g = 1.f;  // 1 / the power of two that this thread's head is multiplied by
         if constexpr (kScaleQ) {
-          float a0 = 0.f, a1 = 0.f;
+          float top = 0.f;
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 x = unpack2<Q>(qa[k][u]);
-              float& a = u & 1 ? a1 : a0;
-              a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
+            for (int u = 0; u < 2; ++u) {
+              const float2 x = unpack2<Q>(qb[k][n][u]);
+              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
             }
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
-            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
-          }
+          for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           // The largest element lands in [2^14, 2^15): float16 keeps bfloat16's bits down to
           // 2^-14, its exponents down to 2^-24.
-          auto to14 = [](float a, float& inverse) {
-            int e = a > 0.f ? 14 - ilogbf(a) : 0;
-            e = min(e, 100);  // (at least 14 - 127)
-            inverse = exp2f((float)-e);
-            return exp2f((float)e);
-          };
-          const float g0 = to14(a0, f0), g1 = to14(a1, f1);
+          const int e = top > 0.f ? min(14 - ilogbf(top), 100) : 0;
+          const float by = exp2f((float)e);
+          g = exp2f((float)-e);
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 x = unpack2<Q>(qa[k][u]);
-              const float g = u & 1 ? g1 : g0;
-              qa[k][u] = pack2<__half>(x.x * g, x.y * g);
+            for (int u = 0; u < 2; ++u) {
+              const float2 x = unpack2<Q>(qb[k][n][u]);
+              qb[k][n][u] = pack2<__half>(x.x * by, x.y * by);
             }
         }
+        f[n][0] = p.scale_log2 * __shfl_sync(0xffffffffu, g, 8 * c4);
+        f[n][1] = p.scale_log2 * __shfl_sync(0xffffffffu, g, 8 * c4 + 4);
       }
-      f0 *= p.scale_log2;
-      f1 *= p.scale_log2;
-      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-      float o[D / 8][4];
+      float m[NT][2], l[NT][2];
+      float o[KS][NT][4];  // 16 elements of D x 8 heads each
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) o[n][u] = 0.f;
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[j][n][u] = 0.f;
+      }
 
       for (int t = s.t0; t < s.t0 + s.nt; ++t, ++slot) {
-        if (mt == 1 && (int)(slot & 1) != slice >> 2) continue;  // tiles alternate
+        if ((int)(slot & (turns - 1)) != turn) continue;
         const uint32_t st = slot % NS;
         wait(full + st, (slot / NS) & 1);
         const uint32_t kt = smem_u32(smem + st * 2 * L::kTile), vt = kt + L::kTile;
         const float* ks = reinterpret_cast<const float*>(smem + L::kScaleOff + st * L::kScales);
-        const int keys = min(s.len - t * kTileKeys, kTileKeys);
-        const int blk0 = mt == 1 ? slice & 3 : slice * blocks;
-        for (int blk = blk0; blk < blk0 + blocks; ++blk) {
-          const int key = blk * 16;
-          const int left = keys - key;  // keys of this step
-          if (left <= 0) break;
-          // ---- logits of 16 keys: two 8-key column tiles
-          float sc[2][4] = {};
-          {
-            const int r = key + ((lane >> 4) << 3) + (lane & 7);
-            if constexpr (!kFp8) {
-#pragma unroll
-              for (int k = 0; k < KS; ++k) {
-                uint32_t b[4];
-                ldsm4(kt + at(r, 2 * k + ((lane >> 3) & 1)), b);
-                mma16816<kBf16>(sc[0], qa[k], b[0], b[1]);
-                mma16816<kBf16>(sc[1], qa[k], b[2], b[3]);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < KS; k += 2) {
-                uint32_t b[4];
-                ldsm4(kt + at(r, k + ((lane >> 3) & 1)), b);
-                mma16816<false>(sc[0], qa[k], cvt_e4m3x2(b[0]), cvt_e4m3x2(b[0] >> 16));
-                mma16816<false>(sc[1], qa[k], cvt_e4m3x2(b[2]), cvt_e4m3x2(b[2] >> 16));
-                mma16816<false>(sc[0], qa[k + 1], cvt_e4m3x2(b[1]), cvt_e4m3x2(b[1] >> 16));
-                mma16816<false>(sc[1], qa[k + 1], cvt_e4m3x2(b[3]), cvt_e4m3x2(b[3] >> 16));
-              }
-            }
-          }
-          // ---- weights; column n * 8 + 2 c4 + e is a key
-          float vs[4], ref_by[4];  // FP8: V's scale of the thread's four keys and its log2
-          if constexpr (kFp8) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int k = key + (u >> 1) * 8 + 2 * c4 + (u & 1);
-              const float kk = ks[k];
-              vs[u] = ks[kTileKeys + k];
-              ref_by[u] = fmaxf(lg2(vs[u]), -64.f);
-              sc[u >> 1][u & 1] *= kk;
-              sc[u >> 1][2 + (u & 1)] *= kk;
-            }
-          }
-          const bool partial = left < 16;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sc[n][e] *= f0;
-              sc[n][2 + e] *= f1;
-              if (partial && n * 8 + 2 * c4 + e >= left) {
-                sc[n][e] = -INFINITY;
-                sc[n][2 + e] = -INFINITY;
-                if constexpr (kFp8) {
-                  vs[2 * n + e] = 0.f;
-                  ref_by[2 * n + e] = 0.f;
-                }
-              }
-            }
-          float t0, t1;
-          if constexpr (kFp8) {
-            t0 = fmaxf(fmaxf(sc[0][0] + ref_by[0], sc[0][1] + ref_by[1]),
-                       fmaxf(sc[1][0] + ref_by[2], sc[1][1] + ref_by[3]));
-            t1 = fmaxf(fmaxf(sc[0][2] + ref_by[0], sc[0][3] + ref_by[1]),
-                       fmaxf(sc[1][2] + ref_by[2], sc[1][3] + ref_by[3]));
-          } else {
-            t0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-            t1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-          }
-          if (__any_sync(0xffffffffu, t0 - m0 > kMoveAt || t1 - m1 > kMoveAt)) {
-#pragma unroll
-            for (int x = 1; x < 4; x <<= 1) {
-              t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-              t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-            }
-            t0 = fmaxf(t0, m0);
-            t1 = fmaxf(t1, m1);
-            const float a0 = ex2_ftz(m0 - finite_ref(t0)), a1 = ex2_ftz(m1 - finite_ref(t1));
-            m0 = t0;
-            m1 = t1;
-            l0 *= a0;
-            l1 *= a1;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[n][0] *= a0;
-              o[n][1] *= a0;
-              o[n][2] *= a1;
-              o[n][3] *= a1;
-            }
-          }
-          const float n0 = -finite_ref(m0), n1 = -finite_ref(m1);
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sc[n][e] = ex2_ftz(sc[n][e] + n0);
-              sc[n][2 + e] = ex2_ftz(sc[n][2 + e] + n1);
-              l0 += sc[n][e];
-              l1 += sc[n][2 + e];
-              if constexpr (kFp8) {
-                sc[n][e] *= vs[2 * n + e];
-                sc[n][2 + e] *= vs[2 * n + e];
-              }
-            }
-          using W = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
-          const uint32_t pa[4] = {pack2<W>(sc[0][0], sc[0][1]), pack2<W>(sc[0][2], sc[0][3]),
-                                  pack2<W>(sc[1][0], sc[1][1]), pack2<W>(sc[1][2], sc[1][3])};
-          // ---- o += weights x V; rows past the sequence's end are cleared (they may hold
-          // anything, and 0 times an infinity is not 0)
-          const int i0 = 2 * c4;
-          const uint32_t v0 = !partial ? ~0u : (i0 < left ? 0xffffu : 0u) | (i0 + 1 < left ? 0xffff0000u : 0u);
-          const uint32_t v1 = !partial ? ~0u : (i0 + 8 < left ? 0xffffu : 0u) | (i0 + 9 < left ? 0xffff0000u : 0u);
-          const int r = key + (((lane >> 3) & 1) << 3) + (lane & 7);
+        const int left = s.len - t * kTileKeys;  // keys of the tile (32 or more: all)
+        // ---- logits: rows i * 16 + r8 (+ 8) are keys, columns heads
+        float sc[2][NT][4] = {};
+        {
+          const int r = (((lane >> 3) & 1) << 3) + (lane & 7);
           if constexpr (!kFp8) {
 #pragma unroll
-            for (int n = 0; n < D / 8; n += 2) {
-              uint32_t b[4];
-              ldsm4t(vt + at(r, n + (lane >> 4)), b);
-              if (partial) {
-                b[0] &= v0;
-                b[1] &= v1;
-                b[2] &= v0;
-                b[3] &= v1;
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a[4];
+                ldsm4(kt + at(16 * i + r, 2 * k + (lane >> 4)), a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<kBf16>(sc[i][n], a, qb[k][n][0], qb[k][n][1]);
               }
-              mma16816<kBf16>(o[n], pa, b[0], b[1]);
-              mma16816<kBf16>(o[n + 1], pa, b[2], b[3]);
-            }
           } else {
 #pragma unroll
-            for (int n = 0; n < D / 16; n += 2) {  // chunks of 16: even and odd elements apart
-              uint32_t b[4];
-              ldsm4t(vt + at(r, n + (lane >> 4)), b);
+            for (int k = 0; k < KS; k += 2)
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                uint32_t e0 = cvt_e4m3x2(__byte_perm(b[2 * u], 0, 0x4420)), e1 = cvt_e4m3x2(__byte_perm(b[2 * u + 1], 0, 0x4420));
-                uint32_t d0 = cvt_e4m3x2(__byte_perm(b[2 * u], 0, 0x4431)), d1 = cvt_e4m3x2(__byte_perm(b[2 * u + 1], 0, 0x4431));
-                if (partial) {
-                  e0 &= v0;
-                  d0 &= v0;
-                  e1 &= v1;
-                  d1 &= v1;
+              for (int i = 0; i < 2; ++i) {
+                uint32_t w[4];
+                ldsm4(kt + at(16 * i + r, k + (lane >> 4)), w);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const uint32_t a[4] = {cvt_e4m3x2(w[2 * u]), cvt_e4m3x2(w[2 * u + 1]),
+                                         cvt_e4m3x2(w[2 * u] >> 16), cvt_e4m3x2(w[2 * u + 1] >> 16)};
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma16816<false>(sc[i][n], a, qb[k + u][n][0], qb[k + u][n][1]);
                 }
-                mma16816<false>(o[2 * (n + u)], pa, e0, e1);
-                mma16816<false>(o[2 * (n + u) + 1], pa, d0, d1);
+              }
+          }
+        }
+        // ---- logits in log2 units; keys past the sequence's end drop out
+        float vs[2][2], ref_by[2][2];  // FP8: V's scales of the thread's keys and their log2
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int key = 16 * i + 8 * u + r8;
+            float kk = 1.f;
+            if constexpr (kFp8) {
+              kk = ks[key];
+              vs[i][u] = ks[kTileKeys + key];
+              ref_by[i][u] = fmaxf(lg2(vs[i][u]), -64.f);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& x = sc[i][n][2 * u + e];
+                x = kFp8 ? (x * kk) * f[n][e] : x * f[n][e];
+                if (key >= left) x = -INFINITY;
+              }
+            if (kFp8 && key >= left) vs[i][u] = ref_by[i][u] = 0.f;
+          }
+        float top[NT][2];
+        bool move = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              x[u] = sc[u >> 1][n][2 * (u & 1) + e];
+              if constexpr (kFp8) x[u] += ref_by[u >> 1][u & 1];
+            }
+            top[n][e] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            move = move || top[n][e] - m[n][e] > kMoveAt;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = top[n][e];
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+              x = fmaxf(x, m[n][e]);
+              const float a = ex2_ftz(m[n][e] - finite_ref(x));
+              m[n][e] = x;
+              l[n][e] *= a;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                o[j][n][e] *= a;
+                o[j][n][2 + e] *= a;
+              }
+            }
+        }
+        // ---- weights, transposed into the second product's K x N operand
+        using W = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+        uint32_t pb[2][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float n0 = -finite_ref(m[n][0]), n1 = -finite_ref(m[n][1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float a = ex2_ftz(sc[i][n][2 * u] + n0), b = ex2_ftz(sc[i][n][2 * u + 1] + n1);
+              l[n][0] += a;
+              l[n][1] += b;
+              if constexpr (kFp8) {
+                a *= vs[i][u];
+                b *= vs[i][u];
+              }
+              pb[i][n][u] = transpose8x8(pack2<W>(a, b));
+            }
+        }
+        // ---- O^T += V^T P^T
+        auto pv = [&](auto tail) {
+          // In the last tile, V's rows past the end are cleared (they may hold anything, and
+          // 0 times an infinity is not 0).
+          auto live = [&](int key) -> uint32_t {
+            return (key < left ? 0xffffu : 0u) | (key + 1 < left ? 0xffff0000u : 0u);
+          };
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t v0 = live(16 * i + 2 * c4), v1 = live(16 * i + 8 + 2 * c4);
+            if constexpr (!kFp8) {
+              const int r = 16 * i + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                uint32_t a[4];
+                ldsm4t(vt + at(r, 2 * j + ((lane >> 3) & 1)), a);
+                if constexpr (decltype(tail)::value) {
+                  a[0] &= v0;
+                  a[1] &= v0;
+                  a[2] &= v1;
+                  a[3] &= v1;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<kBf16>(o[j][n], a, pb[i][n][0], pb[i][n][1]);
+              }
+            } else {
+              const int r = 16 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+              for (int j = 0; j < KS; j += 2) {
+                uint32_t w[4];
+                ldsm4t(vt + at(r, j + (lane >> 4)), w);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  // rows 0..7 are a chunk's even elements, rows 8..15 its odd ones
+                  uint32_t a[4] = {cvt_e4m3x2(__byte_perm(w[2 * u], 0, 0x4420)),
+                                   cvt_e4m3x2(__byte_perm(w[2 * u], 0, 0x4431)),
+                                   cvt_e4m3x2(__byte_perm(w[2 * u + 1], 0, 0x4420)),
+                                   cvt_e4m3x2(__byte_perm(w[2 * u + 1], 0, 0x4431))};
+                  if constexpr (decltype(tail)::value) {
+                    a[0] &= v0;
+                    a[1] &= v0;
+                    a[2] &= v1;
+                    a[3] &= v1;
+                  }
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma16816<false>(o[j + u][n], a, pb[i][n][0], pb[i][n][1]);
+                }
               }
             }
           }
-        }
+        };
+        if (left >= kTileKeys)
+          pv(std::false_type{});
+        else
+          pv(std::true_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + st);
       }
 
       // ---- the pair's results of all warps, joined through shared memory
 #pragma unroll
-      for (int x = 1; x < 4; x <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-      }
-      if (c4 == 0) {
-        red_ml[warp * 16 + r0] = make_float2(m0, l0);
-        red_ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
-      }
-      {
-        // (16-byte chunks xored with the row, r0 = row mod 8, to spread rows over the banks)
-        float* w0 = red + (warp * 16 + r0) * D;
-        float* w1 = w0 + 8 * D;
-        if constexpr (!kFp8) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            const int f = (8 * n + 2 * c4) ^ (r0 << 2);
-            *reinterpret_cast<float2*>(w0 + f) = make_float2(o[n][0], o[n][1]);
-            *reinterpret_cast<float2*>(w1 + f) = make_float2(o[n][2], o[n][3]);
-          }
-        } else {
+        for (int e = 0; e < 2; ++e) {
+          float x = l[n][e];
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            const int f = (16 * n + 4 * c4) ^ (r0 << 2);
-            *reinterpret_cast<float4*>(w0 + f) =
-                make_float4(o[2 * n][0], o[2 * n + 1][0], o[2 * n][1], o[2 * n + 1][1]);
-            *reinterpret_cast<float4*>(w1 + f) =
-                make_float4(o[2 * n][2], o[2 * n + 1][2], o[2 * n][3], o[2 * n + 1][3]);
-          }
+          for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+          const int row = warp * HT + n * 8 + 2 * c4 + e;
+          if (r8 == 0) red_ml[row] = make_float2(m[n][e], x);
+          // (elements xored with the head, to spread the heads over the banks)
+          float* to = red + row * D;
+          const int swz = c4 << 3;
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+            if constexpr (!kFp8) {
+              to[(16 * j + r8) ^ swz] = o[j][n][e];
+              to[(16 * j + 8 + r8) ^ swz] = o[j][n][2 + e];
+            } else {
+              *reinterpret_cast<float2*>(to + ((16 * j + 2 * r8) ^ swz)) =
+                  make_float2(o[j][n][e], o[j][n][2 + e]);
+            }
         }
-      }
       named_bar_sync(1, kConsumers);
       const bool whole = s.nt == s.tiles;
       const size_t head0 = (size_t)s.b * p.h_q + s.h * p.group;  // row of the pair's first head
-      const int part_stride = paged_part_floats(p.group, D);
-      const int my_slot = 2 * blockIdx.x + (s.t0 == 0 && s.first != (long long)blockIdx.x * per ? 1 : 0);
-      float* part = p.partials + (size_t)my_slot * part_stride;
+      const int part_floats = paged_part_floats(p.group, D);
+      // Partial results: slot 2c holds CTA c's first pair, slot 2c + 1 one that starts later.
+      auto part_of = [&](int c, bool later) {
+        return p.partials + (size_t)(2 * c + (later ? 1 : 0)) * part_floats;
+      };
+      float* part = part_of(blockIdx.x, s.t0 == 0 && s.first != (int)blockIdx.x * per);
       auto emit = [&](int hr, int d, float4 v, float m, float l) {  // a finished row's four elements
         const float inv = l > 0.f ? 1.f / l : 0.f;
         uint2 w = make_uint2(pack2<Q>(v.x * inv, v.y * inv), pack2<Q>(v.z * inv, v.w * inv));
@@ -589,70 +615,97 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       };
       for (int e = threadIdx.x; e < p.group * (D / 4); e += kConsumers) {
         const int hr = e / (D / 4), d = e % (D / 4) * 4;
-        float m = -INFINITY;
-        for (int x = 0; x < slices; ++x)
-          m = fmaxf(m, red_ml[((hr >> 4) + mt * x) * 16 + (hr & 15)].x);
-        float l = 0.f;
+        const int swz = ((hr >> 1) & 3) << 3;
+        float mm = -INFINITY;
+        for (int x = 0; x < turns; ++x) mm = fmaxf(mm, red_ml[hr + x * mt * HT].x);
+        float ll = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = 0; x < slices; ++x) {
-          const int row = ((hr >> 4) + mt * x) * 16 + (hr & 15);
+        for (int x = 0; x < turns; ++x) {
+          const int row = hr + x * mt * HT;
           const float2 ml = red_ml[row];
-          const float w = ex2_ftz(ml.x - finite_ref(m));  // 0 for a warp that saw no key
-          const float4 u = *reinterpret_cast<const float4*>(red + row * D + (d ^ ((row & 7) << 2)));
-          l = fmaf(w, ml.y, l);
+          const float w = ex2_ftz(ml.x - finite_ref(mm));  // 0 for a warp that saw no key
+          const float4 u = *reinterpret_cast<const float4*>(red + row * D + (d ^ swz));
+          ll = fmaf(w, ml.y, ll);
           v.x = fmaf(w, u.x, v.x);
           v.y = fmaf(w, u.y, v.y);
           v.z = fmaf(w, u.z, v.z);
           v.w = fmaf(w, u.w, v.w);
         }
         if (whole) {
-          emit(hr, d, v, m, l);
+          emit(hr, d, v, mm, ll);
         } else {
           *reinterpret_cast<float4*>(part + hr * D + d) = v;
-          if (d == 0) *reinterpret_cast<float2*>(part + p.group * D + 2 * hr) = make_float2(m, l);
+          if (d == 0) *reinterpret_cast<float2*>(part + p.group * D + 2 * hr) = make_float2(mm, ll);
         }
       }
+      named_bar_sync(1, kConsumers);  // the buffers are read; the partial result is written
       if (!whole) {
-        const int c0 = (int)(s.first / per), c1 = (int)((s.first + s.tiles - 1) / per);
-        uint32_t* counter = p.counters + (size_t)s.b * p.c.h_kv + s.h;
-        __threadfence();
-        named_bar_sync(1, kConsumers);
+        const int c0 = s.first / per, n = (s.first + s.tiles - 1) / per - c0 + 1;
         if (threadIdx.x == 0) {
-          const bool last = atomicAdd(counter, 1u) == (uint32_t)(c1 - c0);
+          uint32_t* counter = p.counters + (size_t)s.b * p.c.h_kv + s.h;
+          const bool last = atom_add_acq_rel_gpu(counter, 1u) == (uint32_t)(n - 1);
           if (last) *counter = 0;
-          *flag = last;
+          misc[12] = last;
         }
         named_bar_sync(1, kConsumers);
-        if (*flag) {
-          __threadfence();
-          auto slot_of = [&](int c) {
-            return p.partials + (size_t)(2 * c + (c == c0 && s.first != (long long)c * per ? 1 : 0)) * part_stride;
-          };
-          for (int e = threadIdx.x; e < p.group * (D / 4); e += kConsumers) {
-            const int hr = e / (D / 4), d = e % (D / 4) * 4;
-            float m = -INFINITY;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c)
-              m = fmaxf(m, __ldcg(slot_of(c) + p.group * D + 2 * hr));
-            float l = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float* q = slot_of(c);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + p.group * D + 2 * hr));
-              const float4 u = __ldcg(reinterpret_cast<const float4*>(q + hr * D + d));
-              const float w = ex2_ftz(ml.x - finite_ref(m));
-              l = fmaf(w, ml.y, l);
-              v.x = fmaf(w, u.x, v.x);
-              v.y = fmaf(w, u.y, v.y);
-              v.z = fmaf(w, u.z, v.z);
-              v.w = fmaf(w, u.w, v.w);
+        if (misc[12]) {
+          // The last CTA of the pair joins the n partial results.  Heads in batches whose
+          // n x heads weights fit the result buffer.
+          float2* ml = reinterpret_cast<float2*>(red);
+          const int batch = max(1, min(p.group, (int)(L::kRedFloats / 2) / n));
+          const bool later = s.first != c0 * per;
+          for (int h0 = 0; h0 < p.group; h0 += batch) {
+            const int heads = min(batch, p.group - h0);
+            for (int e = threadIdx.x; e < heads * n; e += kConsumers) {
+              const int c = e / heads, hr = e - c * heads;
+              ml[hr * n + c] = __ldcg(reinterpret_cast<const float2*>(
+                  part_of(c0 + c, c == 0 && later) + p.group * D + 2 * (h0 + hr)));
             }
-            emit(hr, d, v, m, l);
+            named_bar_sync(1, kConsumers);
+            for (int hr = warp; hr < heads; hr += 8) {  // a warp per head: weights in place of m
+              float mm = -INFINITY, ll = 0.f;
+              for (int c = lane; c < n; c += 32) mm = fmaxf(mm, ml[hr * n + c].x);
+              mm = warp_max(mm);
+              for (int c = lane; c < n; c += 32) {
+                const float w = ex2_ftz(ml[hr * n + c].x - finite_ref(mm));
+                ll = fmaf(w, ml[hr * n + c].y, ll);
+                ml[hr * n + c].x = w;
+              }
+              ll = warp_sum(ll);
+              __syncwarp();
+              if (lane == 0) red_ml[hr & (8 * HT - 1)] = make_float2(mm, ll);
+              __syncwarp();
+              // the head's D elements, four (two) per lane
+              const float2 t = red_ml[hr & (8 * HT - 1)];
+              constexpr int E = D / 32;
+              float v[E] = {};
+#pragma unroll 8
+              for (int c = 0; c < n; ++c) {
+                const float* q = part_of(c0 + c, c == 0 && later) + (h0 + hr) * D + lane * E;
+                const float w = ml[hr * n + c].x;
+                if constexpr (E == 4) {
+                  const float4 u = __ldcg(reinterpret_cast<const float4*>(q));
+                  v[0] = fmaf(w, u.x, v[0]);
+                  v[1] = fmaf(w, u.y, v[1]);
+                  v[2] = fmaf(w, u.z, v[2]);
+                  v[3] = fmaf(w, u.w, v[3]);
+                } else {
+                  const float2 u = __ldcg(reinterpret_cast<const float2*>(q));
+                  v[0] = fmaf(w, u.x, v[0]);
+                  v[1] = fmaf(w, u.y, v[1]);
+                }
+              }
+              const float inv = t.y > 0.f ? 1.f / t.y : 0.f;
+              uint32_t* out = reinterpret_cast<uint32_t*>(
+                  static_cast<uint8_t*>(p.out) + (head0 + h0 + hr) * (D * 2)) + lane * (E / 2);
+#pragma unroll
+              for (int u = 0; u < E / 2; ++u) out[u] = pack2<Q>(v[2 * u] * inv, v[2 * u + 1] * inv);
+              if (p.lse && lane == 0)
+                p.lse[head0 + h0 + hr] = t.y > 0.f ? (t.x + log2f(t.y)) * kLn2 : -INFINITY;
+            }
+            named_bar_sync(1, kConsumers);
           }
         }
-      } else {
-        named_bar_sync(1, kConsumers);  // the buffers are read before the next pair's results
       }
     }
     __threadfence();  // the results are visible before the next kernel may start
@@ -661,9 +714,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   griddep_launch_dependents();
 }
 
-template <int D, typename Q, bool kFp8>
+template <int D, typename Q, bool kFp8, int NT>
 static cudaError_t launch_paged(const PagedAttnParams& p, cudaStream_t st) {
-  using L = PagedSmem<D, kFp8>;
+  using L = PagedSmem<D, kFp8, NT>;
   const int page = 1 << p.c.page_shift, inner = L::kRowBytes >= 128 ? 128 : L::kRowBytes;
   const int elt = kFp8 ? 1 : 2;
   auto stride = [](int n, int64_t s) { return n > 1 ? (uint64_t)s : uint64_t(16); };
@@ -680,7 +733,7 @@ static cudaError_t launch_paged(const PagedAttnParams& p, cudaStream_t st) {
   if (!make_tmap_nd(&tk, p.c.k, dt, 5, dims, strides, box, sw) ||
       !make_tmap_nd(&tv, p.c.v, dt, 5, dims, strides, box, sw))
     return cudaErrorInvalidValue;
-  auto* kernel = paged_attn_kernel<D, Q, kFp8>;
+  auto* kernel = paged_attn_kernel<D, Q, kFp8, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   const int tiles = (p.c.max_pages * page + kTileKeys - 1) / kTileKeys;
@@ -690,10 +743,18 @@ static cudaError_t launch_paged(const PagedAttnParams& p, cudaStream_t st) {
   return launch_pdl(kernel, dim3(grid), dim3(kPagedThreads), L::kBytes, st, tk, tv, p);
 }
 
+// Groups of up to 8 heads take the kernel with one head tile per warp: half the products
+// and registers of the one with two, which serves larger groups without reading a tile's
+// rows from shared memory once per 8 heads.
+template <int D, typename Q, bool kFp8>
+static cudaError_t launch_paged_n(const PagedAttnParams& p, cudaStream_t st) {
+  return p.group <= 8 ? launch_paged<D, Q, kFp8, 1>(p, st) : launch_paged<D, Q, kFp8, 2>(p, st);
+}
+
 template <int D>
 static cudaError_t launch_paged_d(const PagedAttnParams& p, bool fp8, bool half, cudaStream_t s) {
-  return fp8 ? (half ? launch_paged<D, __half, true>(p, s) : launch_paged<D, __nv_bfloat16, true>(p, s))
-             : (half ? launch_paged<D, __half, false>(p, s) : launch_paged<D, __nv_bfloat16, false>(p, s));
+  return fp8 ? (half ? launch_paged_n<D, __half, true>(p, s) : launch_paged_n<D, __nv_bfloat16, true>(p, s))
+             : (half ? launch_paged_n<D, __half, false>(p, s) : launch_paged_n<D, __nv_bfloat16, false>(p, s));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, int head_dim, int cache_dtype, int q_dtype,
