@@ -441,17 +441,22 @@ def check_device_status(workspace: torch.Tensor, stream=None) -> int:
 _FLOAT16S = {torch.bfloat16: HS2_KV_BF16, torch.float16: HS2_KV_F16}
 
 
-def _launch(what: str, device: torch.device, stream, *args) -> None:
-    """Calls a library function on ``device`` (the tensors' own, which need not be the
+def _launch(what: str, index: int, stream, *args) -> None:
+    """Calls a library function on device ``index`` (the tensors' own, which need not be the
     current one) and on ``stream`` (default: that device's current stream)."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(what, device, stream, *args)
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device != device:
+        raw = torch._C._cuda_getCurrentRawStream(index)  # (no Stream object: these calls are short)
+    elif stream.device_index != index:
         raise ValueError("stream and tensors must be on the same device")
-    _check(getattr(lib(), what)(*args, stream.cuda_stream), what)
+    else:
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        code = getattr(lib(), what)(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = getattr(lib(), what)(*args, raw)
+    if code:
+        raise Hs2Error(code, what)
 
 
 def _new(stream, make, *shape, **kw) -> torch.Tensor:
@@ -462,14 +467,14 @@ def _new(stream, make, *shape, **kw) -> torch.Tensor:
         return make(*shape, **kw)
 
 
-def _check_on(device: torch.device, **tensors) -> None:
+def _check_on(index: int, **tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, like the other tensors")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, like the other tensors")
 
 
-def _check_int32(name: str, t: torch.Tensor, *shape: int) -> None:
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+def _check_int32(name: str, t: torch.Tensor, shape: Tuple[int, ...]) -> None:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
 
 
@@ -481,13 +486,17 @@ def _check_ws(ws: torch.Tensor) -> None:
 def _row_strides(name: str, t: torch.Tensor) -> Tuple[int, ...]:
     """Strides of all axes but the last, which must be contiguous.  Axes of one element get
     the dense stride: theirs is never used and may be anything."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    *strides, last = t.stride()
+    if last != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    got, dense = [], t.shape[-1]
-    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        got.append(s if n > 1 else dense)
-        dense *= n
-    return tuple(reversed(got))
+    shape = t.shape
+    if 1 in shape:
+        dense = shape[-1]
+        for i in range(len(strides) - 1, -1, -1):
+            if shape[i] <= 1:
+                strides[i] = dense
+            dense *= shape[i]
+    return tuple(strides)
 
 
 class PagedCache:
@@ -507,7 +516,8 @@ class PagedCache:
         fp8 = k.dtype == torch.uint8
         if not k.is_cuda:
             raise ValueError("k must be a CUDA tensor")
-        _check_on(k.device, v=v, pages=pages, lens=lens, k_scale=k_scale, v_scale=v_scale)
+        self.index = k.get_device()
+        _check_on(self.index, v=v, pages=pages, lens=lens, k_scale=k_scale, v_scale=v_scale)
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be [num_pages, h_kv, page_size, d] of one type")
         if not fp8 and k.dtype not in _FLOAT16S:
@@ -517,8 +527,8 @@ class PagedCache:
             raise ValueError("k and v must have the same strides")
         if pages.dim() != 2:
             raise ValueError("pages must be int32 [B, max_pages]")
-        _check_int32("pages", pages, *pages.shape)
-        _check_int32("lens", lens, pages.shape[0])
+        _check_int32("pages", pages, pages.shape)
+        _check_int32("lens", lens, pages.shape[:1])
         scale_strides = (0, 0, 0)
         if fp8:
             for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
@@ -537,21 +547,13 @@ class PagedCache:
                                pages.data_ptr(), lens.data_ptr(), *strides, *scale_strides,
                                pages.shape[0], pages.shape[1], k.shape[0], k.shape[2], k.shape[1],
                                k.shape[3], self.dtype)
-
-    @property
-    def batch(self) -> int:
-        return self.pages.shape[0]
-
-    @property
-    def h_kv(self) -> int:
-        return self.k.shape[1]
-
-    @property
-    def head_dim(self) -> int:
-        return self.k.shape[3]
+        self._ref = ctypes.byref(self._struct)
+        self.batch, self.h_kv, self.head_dim = pages.shape[0], k.shape[1], k.shape[3]
+        #: types of the rows and queries that go with this cache
+        self.row_dtypes = tuple(_FLOAT16S) if fp8 else (k.dtype,)
 
     def ref(self):
-        return ctypes.byref(self._struct)
+        return self._ref
 
 
 def paged_workspace(cache: PagedCache, h_q: int = 0) -> torch.Tensor:
@@ -563,16 +565,19 @@ def paged_workspace(cache: PagedCache, h_q: int = 0) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
 
 
-def _check_rows(names: Tuple[str, str], k: torch.Tensor, v: torch.Tensor, cache: PagedCache):
-    """Packed rows of a paged cache: their type code and strides."""
-    want = "bfloat16 or float16" if cache.dtype == HS2_KV_FP8_E4M3 else "the cache's type"
+def _check_rows(k_name: str, v_name: str, k: torch.Tensor, v: torch.Tensor, cache: PagedCache,
+                ws: torch.Tensor):
+    """Packed rows of a paged cache (and the workspace): their type code and strides."""
     if k.dim() != 3 or k.shape[1:] != (cache.h_kv, cache.head_dim) or v.shape != k.shape \
-            or v.dtype != k.dtype or k.dtype not in _FLOAT16S \
-            or (cache.dtype != HS2_KV_FP8_E4M3 and _FLOAT16S[k.dtype] != cache.dtype):
-        raise ValueError(f"{names[0]} and {names[1]} must be [T, h_kv, d] of {want}")
-    strides = _row_strides(names[0], k)
-    if strides != _row_strides(names[1], v):
-        raise ValueError(f"{names[0]} and {names[1]} must have the same strides")
+            or v.dtype != k.dtype or k.dtype not in cache.row_dtypes:
+        raise ValueError(f"{k_name} and {v_name} must be [T, {cache.h_kv}, {cache.head_dim}] of "
+                         f"one type of {cache.row_dtypes}")
+    strides = _row_strides(k_name, k)
+    if strides != (_row_strides(v_name, v) if v.stride() != k.stride() else strides):
+        raise ValueError(f"{k_name} and {v_name} must have the same strides")
+    if not k.get_device() == v.get_device() == ws.get_device() == cache.index:
+        raise ValueError(f"{k_name}, {v_name} and the workspace must be on the cache's device")
+    _check_ws(ws)
     return _FLOAT16S[k.dtype], strides
 
 
@@ -583,12 +588,11 @@ def paged_kv_write(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedCache,
     scale, when the cache is FP8).  ``cache.lens`` counts them already: token i of the n_b of
     sequence b goes to position lens[b] - n_b + i.  cu_new int32 [B + 1]: the sequences'
     ranges of tokens; None: T / B tokens each."""
-    dtype, strides = _check_rows(("k_new", "v_new"), k_new, v_new, cache)
-    _check_on(cache.k.device, k_new=k_new, v_new=v_new, workspace=workspace, cu_new=cu_new)
-    _check_ws(workspace)
+    dtype, strides = _check_rows("k_new", "v_new", k_new, v_new, cache, workspace)
     if cu_new is not None:
-        _check_int32("cu_new", cu_new, cache.batch + 1)
-    _launch("hs2_paged_kv_write", cache.k.device, stream, k_new.data_ptr(), v_new.data_ptr(),
+        _check_int32("cu_new", cu_new, (cache.batch + 1,))
+        _check_on(cache.index, cu_new=cu_new)
+    _launch("hs2_paged_kv_write", cache.index, stream, k_new.data_ptr(), v_new.data_ptr(),
             dtype, *strides, k_new.shape[0], _ptr(cu_new), cache.ref(), workspace.data_ptr(),
             workspace.numel())
 
@@ -602,9 +606,10 @@ def paged_kv_read(cache: PagedCache, cu: torch.Tensor, workspace: torch.Tensor,
     [n_tokens, h_kv, d]: ``k_out`` and ``v_out``, or new tensors of ``n_tokens`` rows (None:
     cu[-1], which waits for the device) of ``dtype`` (None: the cache's type, bfloat16 when
     FP8), zero where no row is read."""
-    _check_int32("cu", cu, cache.batch + 1)
+    _check_int32("cu", cu, (cache.batch + 1,))
     if start is not None:
-        _check_int32("start", start, cache.batch)
+        _check_int32("start", start, (cache.batch,))
+    _check_on(cache.index, cu=cu, start=start)
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     if k_out is None:
@@ -614,17 +619,15 @@ def paged_kv_read(cache: PagedCache, cu: torch.Tensor, workspace: torch.Tensor,
             dtype = torch.bfloat16 if cache.dtype == HS2_KV_FP8_E4M3 else cache.k.dtype
         k_out, v_out = (_new(stream, torch.zeros, n_tokens, cache.h_kv, cache.head_dim,
                              dtype=dtype, device=cache.k.device) for _ in range(2))
-    code, strides = _check_rows(("k_out", "v_out"), k_out, v_out, cache)
-    _check_on(cache.k.device, cu=cu, start=start, k_out=k_out, v_out=v_out, workspace=workspace)
-    _check_ws(workspace)
-    _launch("hs2_paged_kv_read", cache.k.device, stream, cache.ref(), cu.data_ptr(), _ptr(start),
+    code, strides = _check_rows("k_out", "v_out", k_out, v_out, cache, workspace)
+    _launch("hs2_paged_kv_read", cache.index, stream, cache.ref(), cu.data_ptr(), _ptr(start),
             k_out.shape[0], k_out.data_ptr(), v_out.data_ptr(), code, *strides,
             workspace.data_ptr(), workspace.numel())
     return k_out, v_out
 
 
-def _check_out(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, *shape: int) -> None:
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous()):
+def _check_out(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
 
 
@@ -636,15 +639,15 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, workspace: Optional[torch.Ten
     h // (h_q // h_kv)), any strides with a contiguous last axis.  Returns (out, lse): out
     like q and dense, lse float32 [B, h_q]; 0 and -inf for an empty sequence."""
     if q.dim() != 3 or q.shape[0] != cache.batch or q.shape[2] != cache.head_dim \
-            or q.dtype not in _FLOAT16S \
-            or (cache.dtype != HS2_KV_FP8_E4M3 and _FLOAT16S[q.dtype] != cache.dtype):
+            or q.dtype not in cache.row_dtypes:
         raise ValueError("queries must be [B, h_q, d] of the cache's type (bfloat16 or float16 "
                          "for FP8)")
-    B, h_q, d = q.shape
+    shape = q.shape
+    B, h_q, d = shape
     strides = _row_strides("q", q)
-    _check_out("out", out, q.dtype, B, h_q, d)
-    _check_out("lse", lse, torch.float32, B, h_q)
-    _check_on(cache.k.device, q=q, out=out, lse=lse, workspace=workspace)
+    _check_out("out", out, q.dtype, shape)
+    _check_out("lse", lse, torch.float32, shape[:2])
+    _check_on(cache.index, q=q, out=out, lse=lse, workspace=workspace)
     if workspace is None:
         n = lib().hs2_paged_workspace_bytes(cache.ref(), h_q)
         if n == 0:
@@ -656,7 +659,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, workspace: Optional[torch.Ten
     if lse is None and want_lse:
         lse = _new(stream, torch.empty, B, h_q, dtype=torch.float32, device=q.device)
     sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
-    _launch("hs2_paged_attn", q.device, stream, q.data_ptr(), _FLOAT16S[q.dtype], h_q, *strides,
+    _launch("hs2_paged_attn", cache.index, stream, q.data_ptr(), _FLOAT16S[q.dtype], h_q, *strides,
             cache.ref(), sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
             workspace.numel())
     return out, lse
@@ -686,15 +689,17 @@ def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     if cu_q.dim() != 1 or cu_q.shape[0] < 2:
         raise ValueError("cu_q must be int32 [B + 1]")
     B = cu_q.shape[0] - 1
-    _check_int32("cu_q", cu_q, B + 1)
-    _check_int32("cu_k", cu_k, B + 1)
-    tq, h_q, d = q.shape
+    _check_int32("cu_q", cu_q, (B + 1,))
+    if cu_k is not cu_q:
+        _check_int32("cu_k", cu_k, (B + 1,))
+    shape, index = q.shape, q.get_device()
+    tq, h_q, d = shape
     q_strides, kv_strides = _row_strides("q", q), _row_strides("k", k)
-    if kv_strides != _row_strides("v", v):
+    if kv_strides != (_row_strides("v", v) if v.stride() != k.stride() else kv_strides):
         raise ValueError("k and v must have the same strides")
-    _check_out("out", out, q.dtype, tq, h_q, d)
-    _check_out("lse", lse, torch.float32, tq, h_q)
-    _check_on(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, workspace=workspace)
+    _check_out("out", out, q.dtype, shape)
+    _check_out("lse", lse, torch.float32, shape[:2])
+    _check_on(index, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, workspace=workspace)
     if workspace is None:
         workspace = _new(stream, packed_workspace, q.device)
     _check_ws(workspace)
@@ -706,6 +711,6 @@ def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     args = Packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
                   *q_strides, *kv_strides, tq, k.shape[0], B, h_q, k.shape[1], d,
                   _FLOAT16S[q.dtype])
-    _launch("hs2_packed_attn", q.device, stream, ctypes.byref(args), sm_scale, out.data_ptr(),
+    _launch("hs2_packed_attn", index, stream, ctypes.byref(args), sm_scale, out.data_ptr(),
             _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out, lse
