@@ -106,6 +106,29 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
   return w;
 }
+// Element-wise products and sums of two float32 at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 c;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(c))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return c;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 c;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(c))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return c;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 d) {
+  float2 c;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(c))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(d)));
+  return c;
+}
 // Two E4M3 codes (the low 16 bits) as float16, exactly.
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
   const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);

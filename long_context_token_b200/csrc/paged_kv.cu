@@ -4,14 +4,21 @@
 // Both only move bytes: per row of d elements 2d bytes on the packed side and 2d (16-bit)
 // or d + 4 (E4M3 code and float32 scale) in the pages.  A CTA takes a run of tokens: one
 // thread per token first looks up the token's sequence, position and page (four dependent
-// loads), then all threads move the run's rows, 16 bytes of the packed side per thread, so
-// a row is one to two 128-byte lines and the lookups are paid once per token, not per head.
+// loads), once for all its heads.  Then a thread moves 16 elements of the K row and of the V
+// row of a (token, head) pair at a time and loads the next pair before it converts and
+// stores this one; an E4M3 row is a whole number of 16-byte pieces.
+//
+// The quotient x / s only decides a code of 4 significant bits, so instead of dividing (10
+// instructions an element, which then bound the kernel) x is multiplied by 1 / s rounded and
+// widened a little both ways; where the two ends give the same code, so does the quotient,
+// and only the others are divided out (about one in a thousand bfloat16 elements).
 #include "paged.cuh"
 
 namespace hs2 {
 
 constexpr int kMoveThreads = 256;
-constexpr int kMaxTokensPerCta = 32;
+constexpr int kMaxTokensPerCta = 512;
+constexpr int kMoveCtasPerSm = 3;
 
 struct TokenSlot {
   int page;  // -1: nothing to move for this token
@@ -57,73 +64,148 @@ __device__ __forceinline__ TokenSlot token_slot(const PagedMoveParams& p, int t)
   return s;
 }
 
+// The E4M3 codes of x[0..3] / s (IEEE float32 quotients, rounded to nearest even, saturating).
+// r = 1 / s rounded has a relative error of at most 2^-24, each rounded product the same: r
+// made smaller and larger by 2^-21 brackets the quotient, and the conversion is monotone.
+// (`tiny`: s so small that r may overflow.)
+__device__ __forceinline__ uint32_t e4m3_pair(float2 y) {
+  return __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e4m3_of_4(const float2 (&x)[2], float s, float2 below,
+                                              float2 above, bool tiny) {
+  const uint32_t lo = e4m3_pair(mul2(x[0], below)) | (e4m3_pair(mul2(x[1], below)) << 16);
+  const uint32_t hi = e4m3_pair(mul2(x[0], above)) | (e4m3_pair(mul2(x[1], above)) << 16);
+  if (lo == hi && !tiny) return lo;
+  return e4m3_pair(make_float2(__fdiv_rn(x[0].x, s), __fdiv_rn(x[0].y, s))) |
+         (e4m3_pair(make_float2(__fdiv_rn(x[1].x, s), __fdiv_rn(x[1].y, s))) << 16);
+}
+// The larger magnitudes of two 16-bit pairs, element by element.
+template <typename T>
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&a)),
+                              __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  } else {
+    const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+}
+
 // D: head_dim; T: the packed rows' type; kFp8: the cache holds E4M3 codes and scales.
 template <int D, typename T, bool kFp8, bool kWrite>
-__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(PagedMoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kernel(PagedMoveParams p) {
   __shared__ TokenSlot slots[kMaxTokensPerCta];
-  constexpr int kLanes = D / 8;  // threads of one row, 16 bytes each
+  constexpr int kLanes = D / 16;  // threads of one pair of rows, 16 elements each
+  constexpr int kStep = kMoveThreads / kLanes;
+  constexpr int kCells = kFp8 && !kWrite ? 1 : 2;  // 16-byte pieces read per row and thread
   griddep_wait();
   const int t0 = blockIdx.x * p.tokens_per_cta;
   const int nt = min(p.tokens_per_cta, p.n_tokens - t0);
-  if (threadIdx.x < nt) slots[threadIdx.x] = token_slot<kWrite>(p, t0 + threadIdx.x);
+  for (int t = threadIdx.x; t < nt; t += kMoveThreads) slots[t] = token_slot<kWrite>(p, t0 + t);
   __syncthreads();
-  const int c = threadIdx.x % kLanes;
-  const int rows = nt * p.c.h_kv * 2;  // (token, head, K or V)
-  // (every group of kLanes threads goes through the same number of rows or stops as one)
-  for (int r = threadIdx.x / kLanes; r < rows; r += kMoveThreads / kLanes) {
-    const int th = r >> 1, i = th / p.c.h_kv, h = th - i * p.c.h_kv;
-    const bool is_v = r & 1;
-    const TokenSlot s = slots[i];
-    if (s.page < 0) continue;
-    uint8_t* row = (is_v ? p.c.v : p.c.k) + s.page * p.c.page_stride + h * p.c.head_stride +
-                   s.row * p.c.row_stride;
-    const int64_t packed = (int64_t)(t0 + i) * p.token_stride + h * p.head_stride + c * 16;
-    float* sc = kFp8 ? (is_v ? p.c.v_scale : p.c.k_scale) + s.page * p.c.sc_page +
-                           h * p.c.sc_head + s.row * p.c.sc_row
-                     : nullptr;
-    if constexpr (kWrite) {
-      const uint4 w = *reinterpret_cast<const uint4*>((is_v ? p.v_src : p.k_src) + packed);
-      if constexpr (!kFp8) {
-        *reinterpret_cast<uint4*>(row + c * 16) = w;
-      } else {
-        const float2 x[4] = {unpack2<T>(w.x), unpack2<T>(w.y), unpack2<T>(w.z), unpack2<T>(w.w)};
-        float amax = 0.f;
+  const int c = threadIdx.x % kLanes, h_kv = p.c.h_kv;
+  const int step_i = kStep / h_kv, step_h = kStep - step_i * h_kv;
+  int i = (int)(threadIdx.x / kLanes) / h_kv, h = (int)(threadIdx.x / kLanes) - i * h_kv;
+
+  struct Pair {
+    bool live;
+    int64_t packed, paged, scale;  // offsets of the rows (this thread's piece) and of the scale
+    uint4 k[kCells], v[kCells];
+    float ks, vs;
+  };
+  auto fetch = [&](Pair& x) {  // the pair (i, h), and on to this thread's next one
+    x.live = i < nt;
+    if (x.live) {
+      const TokenSlot s = slots[i];
+      x.live = s.page >= 0;
+      if (x.live) {
+        x.packed = (int64_t)(t0 + i) * p.token_stride + h * p.head_stride + c * 32;
+        x.paged = s.page * p.c.page_stride + h * p.c.head_stride + s.row * p.c.row_stride +
+                  c * (kFp8 ? 16 : 32);
+        if constexpr (kFp8) x.scale = s.page * p.c.sc_page + h * p.c.sc_head + s.row * p.c.sc_row;
+        const uint4* k = reinterpret_cast<const uint4*>(kWrite ? p.k_src + x.packed : p.c.k + x.paged);
+        const uint4* v = reinterpret_cast<const uint4*>(kWrite ? p.v_src + x.packed : p.c.v + x.paged);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
-        const uint32_t mask = ((kLanes == 32 ? 0u : 1u << kLanes) - 1u)
-                              << ((threadIdx.x & 31) / kLanes * kLanes);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-          amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-        const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-        uint32_t code[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          code[e] = __nv_cvt_float2_to_fp8x2(
-              make_float2(__fdiv_rn(x[e].x, scale), __fdiv_rn(x[e].y, scale)), __NV_SATFINITE,
-              __NV_E4M3);
-        *reinterpret_cast<uint2*>(row + c * 8) =
-            make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
-        if (c == 0) *sc = scale;
-      }
-    } else {
-      uint4 w;
-      if constexpr (!kFp8) {
-        w = *reinterpret_cast<const uint4*>(row + c * 16);
-      } else {
-        const uint2 code = *reinterpret_cast<const uint2*>(row + c * 8);
-        const float scale = *sc;
-        const uint32_t two[4] = {code.x & 0xffffu, code.x >> 16, code.y & 0xffffu, code.y >> 16};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = __half22float2(e4m3x2_to_half2(two[e]));
-          o[e] = pack2<T>(x.x * scale, x.y * scale);
+        for (int u = 0; u < kCells; ++u) {
+          x.k[u] = k[u];
+          x.v[u] = v[u];
         }
-        w = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (kFp8 && !kWrite) {
+          x.ks = p.c.k_scale[x.scale];
+          x.vs = p.c.v_scale[x.scale];
+        }
       }
-      *reinterpret_cast<uint4*>((is_v ? p.v_dst : p.k_dst) + packed) = w;
     }
+    i += step_i;
+    h += step_h;
+    if (h >= h_kv) {
+      h -= h_kv;
+      ++i;
+    }
+  };
+  auto quantise = [&](const uint4 (&w)[kCells], uint8_t* row, float* scale, uint32_t mask) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = absmax2<T>(top, u[e]);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+      top = absmax2<T>(top, __shfl_xor_sync(mask, top, o));
+    const float2 both = unpack2<T>(top);
+    const float amax = fmaxf(both.x, both.y);
+    const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    const float r = __frcp_rn(s);
+    const float lo = r * (1.f - 0x1p-21f), hi = r * (1.f + 0x1p-21f);
+    const float2 below = make_float2(lo, lo), above = make_float2(hi, hi);
+    const bool tiny = !(s > 1e-30f);
+    uint32_t code[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x[2] = {unpack2<T>(u[2 * e]), unpack2<T>(u[2 * e + 1])};
+      code[e] = e4m3_of_4(x, s, below, above, tiny);
+    }
+    *reinterpret_cast<uint4*>(row) = make_uint4(code[0], code[1], code[2], code[3]);
+    if (c == 0) *scale = s;
+  };
+  auto widen = [&](const uint4 (&w)[kCells], float s, uint8_t* row) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 x = __half22float2(e4m3x2_to_half2((u[e >> 1] >> (16 * (e & 1))) & 0xffffu));
+      o[e] = pack2<T>(x.x * s, x.y * s);
+    }
+    reinterpret_cast<uint4*>(row)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(row)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  };
+  auto put = [&](const Pair& x) {
+    if (!x.live) return;  // (the threads of a pair are live together)
+    uint8_t* k = kWrite ? p.c.k + x.paged : p.k_dst + x.packed;
+    uint8_t* v = kWrite ? p.c.v + x.paged : p.v_dst + x.packed;
+    if constexpr (!kFp8) {
+#pragma unroll
+      for (int u = 0; u < kCells; ++u) {
+        reinterpret_cast<uint4*>(k)[u] = x.k[u];
+        reinterpret_cast<uint4*>(v)[u] = x.v[u];
+      }
+    } else if constexpr (kWrite) {
+      const uint32_t mask = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
+      quantise(x.k, k, p.c.k_scale + x.scale, mask);
+      quantise(x.v, v, p.c.v_scale + x.scale, mask);
+    } else {
+      widen(x.k, x.ks, k);
+      widen(x.v, x.vs, v);
+    }
+  };
+  Pair a, b;
+  fetch(a);
+  for (int u = threadIdx.x / kLanes; u < nt * h_kv; u += 2 * kStep) {
+    fetch(b);
+    put(a);
+    fetch(a);
+    put(b);
   }
   __threadfence();  // the rows are visible before the next kernel may start
   griddep_launch_dependents();
@@ -132,9 +214,10 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(PagedMoveParam
 template <bool kWrite>
 static cudaError_t launch_move(PagedMoveParams p, int head_dim, int cache_dtype, int row_dtype,
                                cudaStream_t s) {
-  // About four CTAs per SM before a CTA takes a second token.
-  int per = p.n_tokens / (4 * device_sm_count());
-  p.tokens_per_cta = per < 1 ? 1 : per > kMaxTokensPerCta ? kMaxTokensPerCta : per;
+  // One run of tokens for every CTA that fits the GPU: the look-ups' latency is paid once.
+  const int ctas = kMoveCtasPerSm * device_sm_count();
+  const int per = (p.n_tokens + ctas - 1) / ctas;
+  p.tokens_per_cta = per > kMaxTokensPerCta ? kMaxTokensPerCta : per;
   const dim3 grid((p.n_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta), block(kMoveThreads);
   const bool fp8 = cache_dtype == HS2_KV_FP8_E4M3, half = row_dtype == HS2_KV_F16;
   // 16-bit rows are copied as they are, whichever of the two types they hold.

@@ -206,6 +206,38 @@ def test_write_and_read(lens, new, kv, src, h_kv, d, page, layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("src", ["bf16", "f16"])
+def test_quotients_at_the_middle_between_codes(src):
+    """Rows of every 16-bit mantissa against maxima of every mantissa and many sizes: quotients
+    at and next to ties, below the normal codes, and scales near the ends of float32."""
+    dt = TYPES[src]
+    bits = 7 if src == "bf16" else 10
+    mant = 1 + torch.arange(2 ** bits) / 2.0 ** bits
+    rows = []
+    g = torch.Generator().manual_seed(19)
+    for e in ([-126, -110, -60, 0, 100, 127] if src == "bf16" else [-14, -8, 0, 15]):
+        for _ in range(40):
+            top = mant[torch.randint(2 ** bits, (1,), generator=g)] * 2.0 ** e
+            shift = torch.randint(0, 18, (128,), generator=g)
+            x = mant[torch.randint(2 ** bits, (128,), generator=g)].double() * 2.0 ** (e - 1 - shift.double())
+            x[5] = top
+            x[6] = -top / 2
+            x[7] = 0
+            rows.append((x * torch.where(torch.rand(128, generator=g) < 0.5, -1.0, 1.0)).to(dt))
+    x = torch.stack(rows)[:, None]
+    n = x.shape[0]
+    pool = Pool([n], 1, 128, 64, "fp8", seed=20, empty=True)
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache)
+    hs2.paged_kv_write(x.to(DEV), x.flip(0).contiguous().to(DEV), cache, ws)
+    pg, r = pool.at(0, 0, n)
+    for got, scale, want in ((cache.k, cache.k_scale, x), (cache.v, cache.v_scale, x.flip(0))):
+        codes, s = quantise(want)
+        assert same(scale.cpu()[pg, :, r], s)
+        assert torch.equal(got.cpu()[pg, :, r], codes)
+
+
+@pytest.mark.gpu
 def test_uniform_write_is_the_packed_one():
     lens, n = [40, 9, 1024], 3
     a, b = (Pool(lens, 2, 128, 32, "fp8", seed=3, empty=True) for _ in range(2))
