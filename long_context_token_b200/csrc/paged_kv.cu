@@ -8,10 +8,12 @@
 // row of a (token, head) pair at a time and loads the next pair before it converts and
 // stores this one; an E4M3 row is a whole number of 16-byte pieces.
 //
-// The quotient x / s only decides a code of 4 significant bits, so instead of dividing (10
-// instructions an element, which then bound the kernel) x is multiplied by 1 / s rounded and
-// widened a little both ways; where the two ends give the same code, so does the quotient,
-// and only the others are divided out (about one in a thousand bfloat16 elements).
+// A division per element (the library's takes some 10 instructions, most of them branches
+// here) would bound the kernel, so the quotients of a row, which share their divisor, are
+// formed from its reciprocal and corrected twice by their remainder: Markstein's method
+// ("Computation of elementary functions on the IBM RISC System/6000 processor", 1990), which
+// gives the correctly rounded quotient from a quotient within one unit in the last place and
+// the correctly rounded reciprocal.
 #include "paged.cuh"
 
 namespace hs2 {
@@ -64,20 +66,18 @@ __device__ __forceinline__ TokenSlot token_slot(const PagedMoveParams& p, int t)
   return s;
 }
 
-// The E4M3 codes of x[0..3] / s (IEEE float32 quotients, rounded to nearest even, saturating).
-// r = 1 / s rounded has a relative error of at most 2^-24, each rounded product the same: r
-// made smaller and larger by 2^-21 brackets the quotient, and the conversion is monotone.
-// (`tiny`: s so small that r may overflow.)
+// Two E4M3 codes, rounded to nearest even, saturating.
 __device__ __forceinline__ uint32_t e4m3_pair(float2 y) {
   return __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t e4m3_of_4(const float2 (&x)[2], float s, float2 below,
-                                              float2 above, bool tiny) {
-  const uint32_t lo = e4m3_pair(mul2(x[0], below)) | (e4m3_pair(mul2(x[1], below)) << 16);
-  const uint32_t hi = e4m3_pair(mul2(x[0], above)) | (e4m3_pair(mul2(x[1], above)) << 16);
-  if (lo == hi && !tiny) return lo;
-  return e4m3_pair(make_float2(__fdiv_rn(x[0].x, s), __fdiv_rn(x[0].y, s))) |
-         (e4m3_pair(make_float2(__fdiv_rn(x[1].x, s), __fdiv_rn(x[1].y, s))) << 16);
+// -x / s, correctly rounded, from nr = -1 / s rounded: the product is within 1.5 units in the
+// last place, so within one after the first correction and rounded correctly after the
+// second.  (The negated quotient keeps the sign of zeros through the corrections.)  Every
+// remainder that matters is exact while s is at least 2^-60; smaller rows are divided out.
+__device__ __forceinline__ float2 minus_quotient(float2 x, float2 s, float2 nr) {
+  float2 y = mul2(x, nr);
+  y = fma2(fma2(y, s, x), nr, y);
+  return fma2(fma2(y, s, x), nr, y);
 }
 // The larger magnitudes of two 16-bit pairs, element by element.
 template <typename T>
@@ -156,15 +156,21 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
     const float2 both = unpack2<T>(top);
     const float amax = fmaxf(both.x, both.y);
     const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    const float r = __frcp_rn(s);
-    const float lo = r * (1.f - 0x1p-21f), hi = r * (1.f + 0x1p-21f);
-    const float2 below = make_float2(lo, lo), above = make_float2(hi, hi);
-    const bool tiny = !(s > 1e-30f);
+    const float nr = -__frcp_rn(s);
+    const float2 s2 = make_float2(s, s), nr2 = make_float2(nr, nr);
     uint32_t code[4];
+    if (s >= 0x1p-60f) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 x[2] = {unpack2<T>(u[2 * e]), unpack2<T>(u[2 * e + 1])};
-      code[e] = e4m3_of_4(x, s, below, above, tiny);
+      for (int e = 0; e < 4; ++e)
+        code[e] = (e4m3_pair(minus_quotient(unpack2<T>(u[2 * e]), s2, nr2)) |
+                   (e4m3_pair(minus_quotient(unpack2<T>(u[2 * e + 1]), s2, nr2)) << 16)) ^ 0x80808080u;
+    } else {  // tiny rows, and NaN
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = unpack2<T>(u[2 * e]), z = unpack2<T>(u[2 * e + 1]);
+        code[e] = e4m3_pair(make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s))) |
+                  (e4m3_pair(make_float2(__fdiv_rn(z.x, s), __fdiv_rn(z.y, s))) << 16);
+      }
     }
     *reinterpret_cast<uint4*>(row) = make_uint4(code[0], code[1], code[2], code[3]);
     if (c == 0) *scale = s;

@@ -215,7 +215,7 @@ def test_quotients_at_the_middle_between_codes(src):
     mant = 1 + torch.arange(2 ** bits) / 2.0 ** bits
     rows = []
     g = torch.Generator().manual_seed(19)
-    for e in ([-126, -110, -60, 0, 100, 127] if src == "bf16" else [-14, -8, 0, 15]):
+    for e in ([-126, -110, -60, -51, -40, 0, 100, 127] if src == "bf16" else [-14, -8, 0, 15]):
         for _ in range(40):
             top = mant[torch.randint(2 ** bits, (1,), generator=g)] * 2.0 ** e
             shift = torch.randint(0, 18, (128,), generator=g)
