@@ -20,7 +20,7 @@ namespace hs2 {
 
 constexpr int kMoveThreads = 256;
 constexpr int kMaxTokensPerCta = 512;
-constexpr int kMoveCtasPerSm = 3;
+constexpr int kMoveCtasPerSm = 4;
 
 struct TokenSlot {
   int page;  // -1: nothing to move for this token
@@ -99,7 +99,12 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
   __shared__ TokenSlot slots[kMaxTokensPerCta];
   constexpr int kLanes = D / 16;  // threads of one pair of rows, 16 elements each
   constexpr int kStep = kMoveThreads / kLanes;
-  constexpr int kCells = kFp8 && !kWrite ? 1 : 2;  // 16-byte pieces read per row and thread
+  // A thread's 16 elements are 8 of each half of a row, so that every access of a row's
+  // threads together covers whole 32-byte sectors: a 16-byte piece of each half, or 8 bytes
+  // of codes.
+  constexpr int kRowHalf = D * (kFp8 ? 1 : 2) / 2, kPackedHalf = D;  // bytes
+  using Cell = typename std::conditional<kFp8 && !kWrite, uint2, uint4>::type;  // as read
+  constexpr int kReadHalf = kWrite ? kPackedHalf : kRowHalf;
   griddep_wait();
   const int t0 = blockIdx.x * p.tokens_per_cta;
   const int nt = min(p.tokens_per_cta, p.n_tokens - t0);
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
   struct Pair {
     bool live;
     int64_t packed, paged, scale;  // offsets of the rows (this thread's piece) and of the scale
-    uint4 k[kCells], v[kCells];
+    Cell k[2], v[2];
     float ks, vs;
   };
   auto fetch = [&](Pair& x) {  // the pair (i, h), and on to this thread's next one
@@ -121,16 +126,16 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
       const TokenSlot s = slots[i];
       x.live = s.page >= 0;
       if (x.live) {
-        x.packed = (int64_t)(t0 + i) * p.token_stride + h * p.head_stride + c * 32;
+        x.packed = (int64_t)(t0 + i) * p.token_stride + h * p.head_stride + c * 16;
         x.paged = s.page * p.c.page_stride + h * p.c.head_stride + s.row * p.c.row_stride +
-                  c * (kFp8 ? 16 : 32);
+                  c * (kFp8 ? 8 : 16);
         if constexpr (kFp8) x.scale = s.page * p.c.sc_page + h * p.c.sc_head + s.row * p.c.sc_row;
-        const uint4* k = reinterpret_cast<const uint4*>(kWrite ? p.k_src + x.packed : p.c.k + x.paged);
-        const uint4* v = reinterpret_cast<const uint4*>(kWrite ? p.v_src + x.packed : p.c.v + x.paged);
+        const uint8_t* k = kWrite ? p.k_src + x.packed : p.c.k + x.paged;
+        const uint8_t* v = kWrite ? p.v_src + x.packed : p.c.v + x.paged;
 #pragma unroll
-        for (int u = 0; u < kCells; ++u) {
-          x.k[u] = k[u];
-          x.v[u] = v[u];
+        for (int u = 0; u < 2; ++u) {
+          x.k[u] = *reinterpret_cast<const Cell*>(k + u * kReadHalf);
+          x.v[u] = *reinterpret_cast<const Cell*>(v + u * kReadHalf);
         }
         if constexpr (kFp8 && !kWrite) {
           x.ks = p.c.k_scale[x.scale];
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
       ++i;
     }
   };
-  auto quantise = [&](const uint4 (&w)[kCells], uint8_t* row, float* scale, uint32_t mask) {
+  auto quantise = [&](const Cell (&w)[2], uint8_t* row, float* scale, uint32_t mask) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
     uint32_t top = 0;
 #pragma unroll
@@ -172,10 +177,11 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
                   (e4m3_pair(make_float2(__fdiv_rn(z.x, s), __fdiv_rn(z.y, s))) << 16);
       }
     }
-    *reinterpret_cast<uint4*>(row) = make_uint4(code[0], code[1], code[2], code[3]);
+    *reinterpret_cast<uint2*>(row) = make_uint2(code[0], code[1]);
+    *reinterpret_cast<uint2*>(row + kRowHalf) = make_uint2(code[2], code[3]);
     if (c == 0) *scale = s;
   };
-  auto widen = [&](const uint4 (&w)[kCells], float s, uint8_t* row) {
+  auto widen = [&](const Cell (&w)[2], float s, uint8_t* row) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
     uint32_t o[8];
 #pragma unroll
@@ -183,8 +189,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
       const float2 x = __half22float2(e4m3x2_to_half2((u[e >> 1] >> (16 * (e & 1))) & 0xffffu));
       o[e] = pack2<T>(x.x * s, x.y * s);
     }
-    reinterpret_cast<uint4*>(row)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<uint4*>(row)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(row) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(row + kPackedHalf) = make_uint4(o[4], o[5], o[6], o[7]);
   };
   auto put = [&](const Pair& x) {
     if (!x.live) return;  // (the threads of a pair are live together)
@@ -192,9 +198,9 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
     uint8_t* v = kWrite ? p.c.v + x.paged : p.v_dst + x.packed;
     if constexpr (!kFp8) {
 #pragma unroll
-      for (int u = 0; u < kCells; ++u) {
-        reinterpret_cast<uint4*>(k)[u] = x.k[u];
-        reinterpret_cast<uint4*>(v)[u] = x.v[u];
+      for (int u = 0; u < 2; ++u) {
+        *reinterpret_cast<uint4*>(k + u * kRowHalf) = x.k[u];
+        *reinterpret_cast<uint4*>(v + u * kRowHalf) = x.v[u];
       }
     } else if constexpr (kWrite) {
       const uint32_t mask = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
