@@ -35,9 +35,14 @@ namespace {
 constexpr int kRows = 128;         // query rows per tile (the MMA's M)
 constexpr int kKeys = 128;         // keys per block (the MMA's N, then its K extent)
 constexpr int kSoftmaxThreads = 256;
-constexpr int kPackedThreads = kSoftmaxThreads + 64;
+constexpr int kPackedThreads = kSoftmaxThreads + 128;  // (two of the last four warps idle)
+// Registers per thread: launched with 168 (65536 / 384, in eights), 64512 in all; then the
+// softmax warps take 200 and the others keep 104: 256 x 200 + 128 x 104 = 64512.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 constexpr float kMoveAt = 8.0f;    // log2 units by which a logit may pass the reference
 constexpr float kLn2 = 0.69314718055994531f;
+
+constexpr uint32_t kNothing = 0xfffffffeu, kNoMore = 0xffffffffu;  // to the cleaner
 
 struct Item {
   int n[2];      // key blocks of each tile (0: none)
@@ -59,37 +64,71 @@ struct PackedSmem {
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kItemOff = kRingOff + kStages * kTile;  // two slots
   static constexpr uint32_t kBarOff = kItemOff + 2 * 64;
-  static constexpr uint32_t kBars = 2 * kStages + 13;
+  static constexpr uint32_t kBars = 2 * kStages + 17;
   static constexpr uint32_t kSlotOff = kBarOff + kBars * 8;
   static constexpr uint32_t kBytes = kSlotOff + 16 + 1024;
   static_assert(sizeof(Item) <= 64 && kBytes <= 227 * 1024, "shared memory budget");
 };
 
-// K-major operand (Q or K tile, boxes of 64 elements, 128-byte swizzle): K step kk of 16.
-__device__ __forceinline__ uint64_t rows_desc(uint32_t tile, int kk) {
-  return smem_desc(tile + (uint32_t)(kk >> 2) * (kRows * 128u) + (uint32_t)(kk & 3) * 32u, 16, 1024,
-                   kSwizzle128B);
+// K-major operand (Q or K tile, boxes of 64 elements, 128-byte swizzle), K step kk of 16, and
+// V tile as the MN-major B operand (N = D, K = keys), keys [16kk, 16kk + 16): descriptors of
+// step 0, and what to add for step kk (the address field counts 16-byte units).
+__device__ __forceinline__ uint64_t rows_desc(uint32_t tile) {
+  return smem_desc(tile, 16, 1024, kSwizzle128B);
 }
-// V tile as the MN-major B operand (N = D, K = keys): K step kk covers keys [16kk, 16kk + 16).
-__device__ __forceinline__ uint64_t v_desc(uint32_t tile, int kk) {
-  return smem_desc(tile + (uint32_t)kk * 16u * 128u, kRows * 128u, 1024, kSwizzle128B);
+__host__ __device__ constexpr uint64_t rows_step(int kk) {
+  return (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4);
 }
+__device__ __forceinline__ uint64_t v_desc(uint32_t tile) {
+  return smem_desc(tile, kRows * 128u, 1024, kSwizzle128B);
+}
+__host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 16 * 128 >> 4); }
 
-__device__ __forceinline__ void zero16(uint8_t* p) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+// 2^x of two numbers at most about 2^7 on the multiply-add pipes: x = n + f with n the nearest
+// integer, 2^f by the polynomial of degree 4 with the least relative error on [-1/2, 1/2]
+// (2.6e-6, from the Remez exchange), n added to its exponent.  Of each kPairsOf pairs of
+// weights kPairsByFma are formed this way: the special-function units give 16 values a clock
+// and SM, the time of the block's MMAs, so they alone would bound the kernel.
+constexpr int kPairsOf = 4, kPairsByFma = 1;
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  x.x = fmaxf(x.x, -126.f);  // (smaller ones give 2^-126: nothing next to the row's sum)
+  x.y = fmaxf(x.y, -126.f);
+  const float2 magic = make_float2(12582912.f, 12582912.f);  // 1.5 x 2^23: its sums are integers
+  const float2 minus = make_float2(-12582912.f, -12582912.f), one = make_float2(-1.f, -1.f);
+  const float2 t = add2(x, magic);
+  const float2 f = fma2(add2(t, minus), one, x);
+  auto both = [](float v) { return make_float2(v, v); };
+  float2 y = fma2(both(0x1.3997d6p-7f), f, both(0x1.ca1444p-5f));
+  y = fma2(y, f, both(0x1.ec06dap-3f));
+  y = fma2(y, f, both(0x1.62e0dcp-1f));
+  y = fma2(y, f, both(0x1.ffffe8p-1f));
+  return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23)));
 }
 
 }  // namespace
 
-// Walks the sequences for the producer warp: work items are numbered sequence by sequence,
-// within one by query block (last first), then K/V head.  Item numbers only grow, so the
-// cursor only moves forward, 32 sequences at a time.
+// Walks the sequences for the producer warp.  Work items are numbered 32 sequences at a time,
+// within them by their number of key blocks, largest first, so that the last items to be
+// handed out are the shortest.  Item numbers only grow, so the cursor only moves forward.
 struct ItemCursor {
-  int b0 = 0;           // first sequence of the current 32
-  uint32_t base = 0;    // items before it
+  int b0 = 0;             // first sequence of the current 32
+  uint32_t base = 0;      // items before it
+  uint32_t total = 0;     // items of the 32
+  int level = 0;          // the current number of key blocks
+  uint32_t above = 0;     // items of the 32 with more key blocks, and with at least as many
+  uint32_t upto = 0;
   int lq = 0, lk = 0, q0 = 0, k0 = 0;  // this lane's sequence
-  uint32_t count = 0, before = 0;      // its items, and the items before it in the 32
-  uint32_t total = 0;   // items of the 32
+  int blocks = 0;         // its query blocks
+  int done = 0, have = 0;  // of them, those with more key blocks than `level`, at least as many
+
+  // How many of this lane's query blocks (the last ones) have at least n key blocks.
+  __device__ int at_least(int n, int tokens_per_item) const {
+    // the block's last token sits at lk - lq + (tokens up to it) - 1 >= (n - 1) * kKeys
+    const int need = n > 0 ? (n - 1) * kKeys + 1 - lk + lq : 0;
+    if (need <= 0) return blocks;
+    return need > lq ? 0 : blocks - (need - 1) / tokens_per_item;
+  }
 
   __device__ void load(const PackedAttnParams& p, int tokens_per_item, int lane) {
     lq = lk = 0;
@@ -103,20 +142,18 @@ struct ItemCursor {
       lq = max(min(b, p.n_q) - q0, 0);
       lk = max(min(d, p.n_k) - k0, 0);
     }
-    count = (uint32_t)((lq + tokens_per_item - 1) / tokens_per_item) * (uint32_t)p.h_kv;
-    uint32_t incl = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    before = incl - count;
-    total = __shfl_sync(0xffffffffu, incl, 31);
+    blocks = (lq + tokens_per_item - 1) / tokens_per_item;
+    total = __reduce_add_sync(0xffffffffu, (uint32_t)blocks) * (uint32_t)p.h_kv;
+    level = __reduce_max_sync(0xffffffffu, blocks > 0 ? (lk + kKeys - 1) / kKeys : 0);
+    done = 0;
+    have = at_least(level, tokens_per_item);
+    above = 0;
+    upto = __reduce_add_sync(0xffffffffu, (uint32_t)have) * (uint32_t)p.h_kv;
   }
 
   // Item number -> item (valid 0 behind the last).  All lanes together, the same number.
-  __device__ Item find(const PackedAttnParams& p, uint32_t item, int tpt, int lane) {
-    while (item - base >= total) {
+  __device__ Item find(const PackedAttnParams& p, uint32_t number, int tpt, int lane) {
+    while (number - base >= total) {
       if (b0 + 32 >= p.batch) {
         Item none = {};
         return none;
@@ -125,17 +162,31 @@ struct ItemCursor {
       b0 += 32;
       load(p, 2 * tpt, lane);
     }
-    const uint32_t at = item - base;
-    const uint32_t owner = __ballot_sync(0xffffffffu, at >= before && at - before < count);
-    const int src = __ffs(owner) - 1;
-    const int s_lq = __shfl_sync(0xffffffffu, lq, src), s_lk = __shfl_sync(0xffffffffu, lk, src);
-    const int s_q0 = __shfl_sync(0xffffffffu, q0, src), s_k0 = __shfl_sync(0xffffffffu, k0, src);
-    const uint32_t in = at - __shfl_sync(0xffffffffu, before, src);
-    const int blocks = (s_lq + 2 * tpt - 1) / (2 * tpt);
-    const int blk = blocks - 1 - (int)(in / (uint32_t)p.h_kv);
+    const uint32_t at = number - base;
+    while (at >= upto) {  // (ends: with level 0, upto is total)
+      --level;
+      done = have;
+      above = upto;
+      have = at_least(level, 2 * tpt);
+      upto = __reduce_add_sync(0xffffffffu, (uint32_t)have) * (uint32_t)p.h_kv;
+    }
+    const uint32_t mine = (uint32_t)(have - done) * (uint32_t)p.h_kv;  // this level's
+    uint32_t before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    before -= mine;
+    const uint32_t in = at - above;
+    const int src = __ffs(__ballot_sync(0xffffffffu, in >= before && in - before < mine)) - 1;
+    auto of = [&](int x) { return __shfl_sync(0xffffffffu, x, src); };
+    const int s_lq = of(lq), s_lk = of(lk), s_q0 = of(q0), s_k0 = of(k0);
+    const uint32_t nth = in - (uint32_t)of((int)before);
+    const int blk = of(blocks) - 1 - of(done) - (int)(nth / (uint32_t)p.h_kv);
     Item it;
     it.valid = 1;
-    it.head = (int)(in % (uint32_t)p.h_kv);
+    it.head = (int)(nth % (uint32_t)p.h_kv);
     const int tok0 = blk * 2 * tpt;  // within the sequence
     it.q_row = s_q0 + tok0;
     it.k_row = s_k0;
@@ -169,12 +220,16 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint64_t* q_full = bars + 2 * NS;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;   // [2] tile's logits complete
-  uint64_t* p_full = q_full + 4;   // [2] tile's weights written
+  uint64_t* p_full = q_full + 4;   // [2] tile's weights written (all)
+  uint64_t* p_half = q_full + 13;  // [2] ... of the block's first 64 keys
   uint64_t* o_full = q_full + 6;   // [2] tile's output complete
   uint64_t* it_full = q_full + 8;  // [2] item slot written
   uint64_t* it_empty = q_full + 10;  // [2] item slot read
   uint64_t* drained = q_full + 12;
+  uint64_t* v_dirty = q_full + 15;  // rows of a V tile to clear, and cleared
+  uint64_t* v_clean = q_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
+  uint32_t* unclean = tmem_slot + 1;  // ring offset of the rows to clear
   auto item_slot = [&](int i) { return reinterpret_cast<Item*>(smem + L::kItemOff + 64 * (i & 1)); };
 
   const int warp = threadIdx.x >> 5, lane = (int)lane_id();
@@ -187,9 +242,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(drained, 1);
+    mbar_init(v_dirty, 1);
+    mbar_init(v_clean, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + t, 1);
       mbar_init(p_full + t, kRows);
+      mbar_init(p_half + t, kRows);
       mbar_init(o_full + t, 1);
       mbar_init(it_full + t, 1);
       mbar_init(it_empty + t, kSoftmaxThreads + 1);
@@ -218,7 +276,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
   };
 
-  if (warp == 9) {
+  if (warp >= 8) {
+    reg_dec<kOtherRegs>();
+    if (warp == 9) {
     // ------------------------------------------------------------ items and loads
     ItemCursor cur;
     cur.load(p, 2 * tpt, lane);
@@ -283,106 +343,132 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         p.sync[1] = 0;
       }
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t id_qk = idesc_f16(kRows, kKeys, kBf16, false, false);
-    constexpr uint32_t id_pv = idesc_f16(kRows, D, kBf16, false, true);
-    const uint32_t q_addr = smem_u32(qs);
-    uint32_t slot = 0, q_loads = 0;
-    uint32_t n_p[2] = {0, 0};  // weights consumed of each tile
-    for (int i = 0; ok; ++i) {
-      wait(it_full + (i & 1), (i >> 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const Item it = *item_slot(i);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(it_empty + (i & 1));
-      if (!it.valid) break;
-      const int blocks = max(it.n[0], it.n[1]);
-      if (blocks == 0) continue;
-      auto qk = [&](int t, uint32_t k_addr) {
-        if (lane == 0) {
+    } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer (one thread)
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f16(kRows, kKeys, kBf16, false, false);
+      constexpr uint32_t id_pv = idesc_f16(kRows, D, kBf16, false, true);
+      const uint64_t qd[2] = {rows_desc(smem_u32(qs)), rows_desc(smem_u32(qs) + L::kTile)};
+      uint32_t slot = 0, q_loads = 0, n_clean = 0;
+      uint32_t n_p[2] = {0, 0};  // weights consumed of each tile
+      auto qk = [&](auto tile, uint64_t kd) {
+        constexpr int t = decltype(tile)::value;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ss(tmem + t * kKeys, rows_desc(q_addr + t * L::kTile, kk), rows_desc(k_addr, kk),
-                       id_qk, kk > 0 ? 1u : 0u);
-          mma_commit(s_full + t);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(tmem + t * kKeys, qd[t] + rows_step(kk), kd + rows_step(kk), id_qk, kk > 0 ? 1u : 0u);
+        mma_commit(s_full + t);
       };
-      auto pv = [&](int t, uint32_t v_addr, int steps, int j) {
-        wait(p_full + t, n_p[t] & 1);
-        ++n_p[t];
-        ok = __all_sync(0xffffffffu, ok);
+      auto pv = [&](auto tile, uint64_t vd, int steps, bool first, bool last) {
+        constexpr int t = decltype(tile)::value;
+        const uint32_t o = tmem + 2 * kKeys + t * kKeys, w = tmem + t * kKeys;
+        wait(p_half + t, n_p[t] & 1);
+        tc_fence_after();
         if (!ok) return;
-        tc_fence_after();
-        if (lane == 0) {
+        if (steps == 8) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
+          wait(p_full + t, n_p[t] & 1);
+          tc_fence_after();
+          if (!ok) return;
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, 1u);
+        } else {
+          wait(p_full + t, n_p[t] & 1);
+          tc_fence_after();
+          if (!ok) return;
           for (int kk = 0; kk < steps; ++kk)
-            mma_f16_ts(tmem + 2 * kKeys + t * kKeys, tmem + t * kKeys + kk * 8, v_desc(v_addr, kk),
-                       id_pv, (j > 0 || kk > 0) ? 1u : 0u);
-          if (j == it.n[t] - 1) mma_commit(o_full + t);
+            mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
         }
+        ++n_p[t];
+        if (last) mma_commit(o_full + t);
       };
-      // Logits of both tiles for the block in ring slot `slot`.
-      auto next_k = [&]() -> uint32_t {
-        wait(full + slot % NS, (slot / NS) & 1);
-        ok = __all_sync(0xffffffffu, ok);
+      const std::integral_constant<int, 0> t0;
+      const std::integral_constant<int, 1> t1;
+      auto next = [&]() -> uint32_t {  // the next ring slot, when it is filled
+        const uint32_t s = slot % NS;
+        wait(full + s, (slot / NS) & 1);
         tc_fence_after();
-        return smem_u32(ring + (slot % NS) * L::kTile);
-      };
-      wait(q_full, q_loads & 1);
-      ++q_loads;
-      uint32_t k_addr = next_k();
-      if (!ok) break;
-      if (it.n[0] > 0) qk(0, k_addr);
-      if (it.n[1] > 0) qk(1, k_addr);
-      if (lane == 0) {
-        mma_commit(empty + slot % NS);
-        if (blocks == 1) mma_commit(q_empty);
-      }
-      ++slot;
-      for (int j = 0; j < blocks && ok; ++j) {
-        const uint32_t v_slot = slot;
-        const uint32_t v_addr = next_k();
         ++slot;
+        return s;
+      };
+      for (int i = 0; ok; ++i) {
+        wait(it_full + (i & 1), (i >> 1) & 1);
         if (!ok) break;
-        // The sequence's last block: MMA steps past its keys are left out, and the rows of
-        // the last step that belong to other sequences are cleared (their weights are 0,
-        // but 0 times an infinity or NaN is not).
-        const int live = min(it.lk - j * kKeys, kKeys);
-        const int steps = (live + 15) >> 4;
-        if (live & 15) {
-          const int rows = 16 - (live & 15);
-          uint8_t* base = ring + (v_slot % NS) * L::kTile + live * 128;
-          for (int e = lane; e < rows * 8 * (D / 64); e += 32)
-            zero16(base + (e >> 3) % rows * 128 + (e >> 3) / rows * L::kBox + (e & 7) * 16);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (j < it.n[0]) pv(0, v_addr, steps, j);
-        uint32_t k_slot = 0;
-        if (j + 1 < blocks && ok) {
-          k_slot = slot;
-          k_addr = next_k();
-          ++slot;
-          if (ok && j + 1 < it.n[0]) qk(0, k_addr);
-        }
-        if (j < it.n[1] && ok) pv(1, v_addr, steps, j);
-        if (lane == 0) mma_commit(empty + v_slot % NS);
-        if (j + 1 < blocks && ok) {
-          if (j + 1 < it.n[1]) qk(1, k_addr);
-          if (lane == 0) {
-            mma_commit(empty + k_slot % NS);
+        const Item it = *item_slot(i);
+        mbar_arrive(it_empty + (i & 1));
+        if (!it.valid) break;
+        const int blocks = max(it.n[0], it.n[1]);
+        if (blocks == 0) continue;
+        wait(q_full, q_loads & 1);
+        ++q_loads;
+        uint32_t ks = next();
+        if (!ok) break;
+        uint64_t kd = rows_desc(smem_u32(ring + ks * L::kTile));
+        if (it.n[0] > 0) qk(t0, kd);
+        if (it.n[1] > 0) qk(t1, kd);
+        mma_commit(empty + ks);
+        if (blocks == 1) mma_commit(q_empty);
+        for (int j = 0; j < blocks && ok; ++j) {
+          const uint32_t vs = next();
+          if (!ok) break;
+          const uint64_t vd = v_desc(smem_u32(ring + vs * L::kTile));
+          // The sequence's last block: MMA steps past its keys are left out, and the rows of
+          // the last step that belong to other sequences are cleared first.
+          const int live = min(it.lk - j * kKeys, kKeys);
+          const int steps = (live + 15) >> 4;
+          if (j == blocks - 1) {  // (the cleaner hears of every item, so that its waits are short)
+            if (n_clean > 0) wait(v_clean, (n_clean - 1) & 1);
+            *unclean = live & 15 ? vs * L::kTile + live * 128 : kNothing;
+            mbar_arrive(v_dirty);
+            ++n_clean;
+            if (live & 15) wait(v_clean, (n_clean - 1) & 1);
+          }
+          if (j < it.n[0] && ok) pv(t0, vd, steps, j == 0, j == it.n[0] - 1);
+          const bool more = j + 1 < blocks;
+          if (more && ok) {
+            ks = next();
+            kd = rows_desc(smem_u32(ring + ks * L::kTile));
+            if (ok && j + 1 < it.n[0]) qk(t0, kd);
+          }
+          if (j < it.n[1] && ok) pv(t1, vd, steps, j == 0, j == it.n[1] - 1);
+          mma_commit(empty + vs);
+          if (more && ok) {
+            if (j + 1 < it.n[1]) qk(t1, kd);
+            mma_commit(empty + ks);
             if (j + 2 == blocks) mma_commit(q_empty);
           }
         }
       }
-    }
-    if (lane == 0) {  // nothing of this CTA's is in flight when the TMEM goes
-      mma_commit(drained);
+      if (n_clean > 0) wait(v_clean, (n_clean - 1) & 1);
+      *unclean = kNoMore;
+      mbar_arrive(v_dirty);
+      mma_commit(drained);  // nothing of this CTA's is in flight when the TMEM goes
       mbar_wait(drained, 0);
+    }
+    __syncwarp();
+    } else if (warp == 10) {
+    // ------------------------------------------------------------ cleaner
+    // Clears the rows of a V tile's last MMA step that lie behind its sequence's end: their
+    // weights are 0, but 0 times another sequence's infinity or NaN is not.
+    for (uint32_t n = 0; ok; ++n) {
+      wait(v_dirty, n & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t from = *reinterpret_cast<volatile uint32_t*>(unclean);
+      if (from == kNoMore) break;
+      const int rows = from == kNothing ? 0 : 16 - (int)((from / 128) & 15);
+      for (int e = lane; e < rows * 8 * (D / 64); e += 32)
+        *reinterpret_cast<uint4*>(ring + from + (e >> 3) % rows * 128 + (e >> 3) / rows * L::kBox +
+                                  (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_clean);
+    }
     }
   } else {
     // ------------------------------------------------------------ softmax
+    reg_inc<kSoftmaxRegs>();
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -446,24 +532,29 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           }
         }
         const float ref = -finite_ref(m);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < kKeys; e += 2) {
-          const float a = ex2_ftz(fmaf(__uint_as_float(s[e]), c, ref));
-          const float b = ex2_ftz(fmaf(__uint_as_float(s[e + 1]), c, ref));
-          sum[e & 2] += a;
-          sum[(e & 2) + 1] += b;
-          s[e >> 1] = pack2<T>(a, b);
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int e = half * 64; e < half * 64 + 64; e += 2) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, ref2);
+            const bool by_fma = e / 2 % kPairsOf >= kPairsOf - kPairsByFma;
+            const float2 w = by_fma ? exp2_fma(x) : make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+            sum[e / 2 & 1] = add2(sum[e / 2 & 1], w);
+            s[e >> 1] = pack2<T>(w.x, w.y);
+          }
+          tmem_st32(ts + half * 32, s + half * 32);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive((half ? p_full : p_half) + t);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(ts, s);
-        tmem_st32(ts + 32, s + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(p_full + t);
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
       }
       if (!ok) break;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool any = seen > 0;
+      const float inv = any ? 1.f / l : 0.f;
       const size_t row = (size_t)(it.q_row + t * tpt + tok) * p.h_q + it.head * p.group + hh;
       uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * (D * 2));
       if (it.n[t] > 0) {
@@ -485,7 +576,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                w[x] = l > 0.f ? pack2<T>(__uint_as_float(o[u + 2 * x]) * inv,
+                w[x] = any ? pack2<T>(__uint_as_float(o[u + 2 * x]) * inv,
                                           __uint_as_float(o[u + 2 * x + 1]) * inv)
                                : 0u;
               out[(e + u) >> 3] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -497,7 +588,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
         for (int e = 0; e < D / 8; ++e) out[e] = make_uint4(0, 0, 0, 0);
       }
-      if (live && p.lse) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (live && p.lse) p.lse[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
     __threadfence();  // the results are visible before the next kernel may start
   }
