@@ -3,20 +3,23 @@
 // A work item is one sequence, one K/V head and 2 x 128 query rows: a row is a (token, head
 // of the group) pair, tokens outer, so the query heads that share a K/V head share its tiles
 // and a short prompt still fills the MMA's 128 rows.  Persistent CTAs, one per SM, take items
-// from a counter, each sequence's longest ones first.  Per 128-key block j and tile t:
+// from a counter, those with the most keys first.  Keys go in steps i of 64; per step and tile t:
 //
-//   S_t[128 x 128]  = Q_t . K_j^T            (smem x smem, D/16 MMAs)
+//   S_t[128 x 64]   = Q_t . K_i^T            (smem x smem, D/16 MMAs)
 //   P_t             = 2^(S_t c - m)          (softmax warps, one thread per row)
-//   O_t[128 x D]   += P_t . V_j              (P_t from TMEM, 128/16 MMAs)
+//   O_t[128 x D]   += P_t . V_i              (P_t from TMEM, 4 MMAs)
 //
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns a row, so the row's maximum and
 //               sum need no shuffle.  The reference m moves only when a logit passes it by
-//               more than 8 (log2 units); O is then rescaled in TMEM, which is safe once
-//               S_t(j) is complete because P_t(j-1) . V ran before it.  P replaces S in TMEM
-//               (two 16-bit weights per column).
-//   warp 8      MMA issuer: Q.K of block j + 1 is issued after P.V of block j of the same
-//               tile, so each tile's softmax runs under the other tile's MMAs.
-//   warp 9      work items and TMA loads: Q (2 x 128 rows), K and V blocks in one ring.
+//               more than 8 (log2 units); O is then rescaled in TMEM, after P(i-1) . V.
+//               P replaces S in TMEM (two 16-bit weights per column).
+//   warp 8      MMA issuer (one thread): each tile has two S buffers, and Q.K of step i + 1
+//               is issued before P.V of step i, so the softmax of a tile never waits for its
+//               own products.  (With 128-key steps S has one buffer, and the chain Q.K,
+//               softmax, P.V of each tile was what bounded the kernel: 1040 us for a
+//               16384-token prompt of 16 heads.)
+//   warp 9      work items and TMA loads: Q (2 x 128 rows), 128-key K and V blocks in a ring.
+//   warp 10     clears V rows of other sequences in a sequence's last block.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product, as the MMA needs;
 // the row sums, references and O stay in float32.
@@ -33,19 +36,17 @@ using namespace sm100;
 namespace {
 
 constexpr int kRows = 128;         // query rows per tile (the MMA's M)
-constexpr int kKeys = 128;         // keys per block (the MMA's N, then its K extent)
+constexpr int kKeys = 128;         // keys per loaded block
+constexpr int kStep = 64;          // keys per step (the MMA's N, then its K extent)
 constexpr int kSoftmaxThreads = 256;
-constexpr int kPackedThreads = kSoftmaxThreads + 128;  // (two of the last four warps idle)
-// Registers per thread: launched with 168 (65536 / 384, in eights), 64512 in all; then the
-// softmax warps take 200 and the others keep 104: 256 x 200 + 128 x 104 = 64512.
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+constexpr int kPackedThreads = kSoftmaxThreads + 96;
 constexpr float kMoveAt = 8.0f;    // log2 units by which a logit may pass the reference
 constexpr float kLn2 = 0.69314718055994531f;
 
 constexpr uint32_t kNothing = 0xfffffffeu, kNoMore = 0xffffffffu;  // to the cleaner
 
 struct Item {
-  int n[2];      // key blocks of each tile (0: none)
+  int n[2];      // key steps of each tile (0: none)
   int tokens[2];  // query tokens of each tile
   int q_row;     // first query token (row of q)
   int pos;       // its position in its sequence
@@ -64,7 +65,7 @@ struct PackedSmem {
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kItemOff = kRingOff + kStages * kTile;  // two slots
   static constexpr uint32_t kBarOff = kItemOff + 2 * 64;
-  static constexpr uint32_t kBars = 2 * kStages + 17;
+  static constexpr uint32_t kBars = 2 * kStages + 21;
   static constexpr uint32_t kSlotOff = kBarOff + kBars * 8;
   static constexpr uint32_t kBytes = kSlotOff + 16 + 1024;
   static_assert(sizeof(Item) <= 64 && kBytes <= 227 * 1024, "shared memory budget");
@@ -196,7 +197,7 @@ struct ItemCursor {
     for (int t = 0; t < 2; ++t) {
       it.tokens[t] = min(max(s_lq - tok0 - t * tpt, 0), tpt);
       const int last = it.pos + t * tpt + it.tokens[t] - 1;  // the tile's last token sees [0, last]
-      it.n[t] = it.tokens[t] > 0 && last >= 0 ? last / kKeys + 1 : 0;
+      it.n[t] = it.tokens[t] > 0 && last >= 0 ? last / kStep + 1 : 0;
     }
     return it;
   }
@@ -219,20 +220,22 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint64_t* empty = bars + NS;
   uint64_t* q_full = bars + 2 * NS;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_full + 2;   // [2] tile's logits complete
-  uint64_t* p_full = q_full + 4;   // [2] tile's weights written (all)
-  uint64_t* p_half = q_full + 13;  // [2] ... of the block's first 64 keys
-  uint64_t* o_full = q_full + 6;   // [2] tile's output complete
-  uint64_t* it_full = q_full + 8;  // [2] item slot written
-  uint64_t* it_empty = q_full + 10;  // [2] item slot read
-  uint64_t* drained = q_full + 12;
-  uint64_t* v_dirty = q_full + 15;  // rows of a V tile to clear, and cleared
-  uint64_t* v_clean = q_full + 16;
+  uint64_t* s_full = q_full + 2;     // [2 tiles][2 buffers] logits complete
+  uint64_t* p_full = q_full + 6;     // [2 tiles][2 buffers] weights written
+  // [2 tiles][2 buffers] a step's product is in the tile's output.  (One barrier per buffer:
+  // who waits for a step has seen the one before the last, so a parity tells its phases apart.)
+  uint64_t* o_done = q_full + 10;
+  uint64_t* it_full = q_full + 14;   // [2] item slot written
+  uint64_t* it_empty = q_full + 16;  // [2] item slot read
+  uint64_t* drained = q_full + 18;
+  uint64_t* v_dirty = q_full + 19;   // rows of a V block to clear, and cleared
+  uint64_t* v_clean = q_full + 20;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   uint32_t* unclean = tmem_slot + 1;  // ring offset of the rows to clear
   auto item_slot = [&](int i) { return reinterpret_cast<Item*>(smem + L::kItemOff + 64 * (i & 1)); };
 
-  const int warp = threadIdx.x >> 5, lane = (int)lane_id();
+  // (shuffled: the compiler then knows that a warp takes one role as a whole)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = (int)lane_id();
   const int tpt = kRows / p.group;  // query tokens per tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -244,11 +247,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     mbar_init(drained, 1);
     mbar_init(v_dirty, 1);
     mbar_init(v_clean, 1);
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 4; ++t) {
       mbar_init(s_full + t, 1);
       mbar_init(p_full + t, kRows);
-      mbar_init(p_half + t, kRows);
-      mbar_init(o_full + t, 1);
+      mbar_init(o_done + t, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
       mbar_init(it_full + t, 1);
       mbar_init(it_empty + t, kSoftmaxThreads + 1);
     }
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S0, S1: 128 columns each; O0, O1: at 256, 256 + 128
+  const uint32_t tmem = *tmem_slot;  // two S buffers of 64 columns per tile; O0, O1 at 256, 256 + 128
   griddep_wait();
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -276,9 +280,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
   };
 
-  if (warp >= 8) {
-    reg_dec<kOtherRegs>();
-    if (warp == 9) {
+  if (warp == 9) {
     // ------------------------------------------------------------ items and loads
     ItemCursor cur;
     cur.load(p, 2 * tpt, lane);
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         mbar_arrive(it_full + (i & 1));
       }
       if (!it.valid) break;
-      const int blocks = max(it.n[0], it.n[1]);
+      const int blocks = (max(it.n[0], it.n[1]) * kStep + kKeys - 1) / kKeys;
       if (lane == 0 && blocks > 0) {
         auto fill = [&](const CUtensorMap* m, int x, int y, int z, int boxes) {
           const uint32_t s = slot % NS;
@@ -343,111 +345,136 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         p.sync[1] = 0;
       }
     }
-    } else if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer (one thread)
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16(kRows, kKeys, kBf16, false, false);
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the loop and one elected thread issues: descriptors and TMEM
+    // addresses then are warp-uniform values, which the MMA takes as they are.  (From a
+    // branch of a single thread each MMA cost about 115 cycles to issue, twice its run time.)
+    {
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        wait(bar, parity);
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      constexpr uint32_t id_qk = idesc_f16(kRows, kStep, kBf16, false, false);
       constexpr uint32_t id_pv = idesc_f16(kRows, D, kBf16, false, true);
       const uint64_t qd[2] = {rows_desc(smem_u32(qs)), rows_desc(smem_u32(qs) + L::kTile)};
       uint32_t slot = 0, q_loads = 0, n_clean = 0;
-      uint32_t n_p[2] = {0, 0};  // weights consumed of each tile
+      uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0};  // products issued of each tile, of all items
       auto qk = [&](auto tile, uint64_t kd) {
         constexpr int t = decltype(tile)::value;
+        const uint32_t buf = n_s[t]++ & 1;
+        const uint32_t d = tm + t * 2 * kStep + buf * kStep;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ss(tmem + t * kKeys, qd[t] + rows_step(kk), kd + rows_step(kk), id_qk, kk > 0 ? 1u : 0u);
-        mma_commit(s_full + t);
-      };
-      auto pv = [&](auto tile, uint64_t vd, int steps, bool first, bool last) {
-        constexpr int t = decltype(tile)::value;
-        const uint32_t o = tmem + 2 * kKeys + t * kKeys, w = tmem + t * kKeys;
-        wait(p_half + t, n_p[t] & 1);
-        tc_fence_after();
-        if (!ok) return;
-        if (steps == 8) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
-          wait(p_full + t, n_p[t] & 1);
-          tc_fence_after();
-          if (!ok) return;
-#pragma unroll
-          for (int kk = 4; kk < 8; ++kk) mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, 1u);
-        } else {
-          wait(p_full + t, n_p[t] & 1);
-          tc_fence_after();
-          if (!ok) return;
-          for (int kk = 0; kk < steps; ++kk)
-            mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ss(d, qd[t] + rows_step(kk), kd + rows_step(kk), id_qk, kk > 0 ? 1u : 0u);
+          mma_commit(s_full + 2 * t + buf);
         }
-        ++n_p[t];
-        if (last) mma_commit(o_full + t);
+        __syncwarp();
+      };
+      auto pv = [&](auto tile, uint64_t vd, int live, bool first) {
+        constexpr int t = decltype(tile)::value;
+        const uint32_t n = n_p[t]++, buf = n & 1;
+        const uint32_t o = tm + 4 * kStep + t * 128, w = tm + t * 2 * kStep + buf * kStep;
+        wait_all(p_full + 2 * t + buf, (n >> 1) & 1);
+        tc_fence_after();
+        if (!ok) return;  // (the caller's loops end with it)
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            if (kk * 16 < live)  // (MMA steps past the sequence's keys are left out)
+              mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
+          mma_commit(o_done + 2 * t + buf);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
       };
       const std::integral_constant<int, 0> t0;
       const std::integral_constant<int, 1> t1;
       auto next = [&]() -> uint32_t {  // the next ring slot, when it is filled
         const uint32_t s = slot % NS;
-        wait(full + s, (slot / NS) & 1);
+        wait_all(full + s, (slot / NS) & 1);
         tc_fence_after();
         ++slot;
         return s;
       };
+      constexpr uint64_t kHalf = (uint64_t)(kStep * 128 >> 4);  // rows 64.. of a K or V block
       for (int i = 0; ok; ++i) {
-        wait(it_full + (i & 1), (i >> 1) & 1);
+        wait_all(it_full + (i & 1), (i >> 1) & 1);
         if (!ok) break;
-        const Item it = *item_slot(i);
-        mbar_arrive(it_empty + (i & 1));
-        if (!it.valid) break;
-        const int blocks = max(it.n[0], it.n[1]);
-        if (blocks == 0) continue;
-        wait(q_full, q_loads & 1);
+        const Item* it = item_slot(i);
+        const int n0 = __shfl_sync(0xffffffffu, it->n[0], 0), n1 = __shfl_sync(0xffffffffu, it->n[1], 0);
+        const int lk = __shfl_sync(0xffffffffu, it->lk, 0);
+        const int valid = __shfl_sync(0xffffffffu, it->valid, 0);
+        if (lane == 0) mbar_arrive(it_empty + (i & 1));
+        if (!valid) break;
+        const int steps = max(n0, n1);
+        if (steps == 0) continue;
+        wait_all(q_full, q_loads & 1);
         ++q_loads;
-        uint32_t ks = next();
+        uint32_t ks = next(), vs = 0;
         if (!ok) break;
-        uint64_t kd = rows_desc(smem_u32(ring + ks * L::kTile));
-        if (it.n[0] > 0) qk(t0, kd);
-        if (it.n[1] > 0) qk(t1, kd);
-        mma_commit(empty + ks);
-        if (blocks == 1) mma_commit(q_empty);
-        for (int j = 0; j < blocks && ok; ++j) {
-          const uint32_t vs = next();
-          if (!ok) break;
-          const uint64_t vd = v_desc(smem_u32(ring + vs * L::kTile));
-          // The sequence's last block: MMA steps past its keys are left out, and the rows of
-          // the last step that belong to other sequences are cleared first.
-          const int live = min(it.lk - j * kKeys, kKeys);
-          const int steps = (live + 15) >> 4;
-          if (j == blocks - 1) {  // (the cleaner hears of every item, so that its waits are short)
-            if (n_clean > 0) wait(v_clean, (n_clean - 1) & 1);
-            *unclean = live & 15 ? vs * L::kTile + live * 128 : kNothing;
-            mbar_arrive(v_dirty);
-            ++n_clean;
-            if (live & 15) wait(v_clean, (n_clean - 1) & 1);
-          }
-          if (j < it.n[0] && ok) pv(t0, vd, steps, j == 0, j == it.n[0] - 1);
-          const bool more = j + 1 < blocks;
-          if (more && ok) {
+        uint64_t kd = rows_desc(smem_u32(ring + ks * L::kTile)), vd = 0;
+        if (n0 > 0) qk(t0, kd);
+        if (n1 > 0) qk(t1, kd);
+        if (steps == 1) {
+          commit(empty + ks);
+          commit(q_empty);
+        }
+        for (int j = 0; j < steps && ok; ++j) {
+          // step j of P.V behind step j + 1 of Q.K
+          const bool more = j + 1 < steps;
+          if ((j & 1) && more) {
             ks = next();
             kd = rows_desc(smem_u32(ring + ks * L::kTile));
-            if (ok && j + 1 < it.n[0]) qk(t0, kd);
           }
-          if (j < it.n[1] && ok) pv(t1, vd, steps, j == 0, j == it.n[1] - 1);
-          mma_commit(empty + vs);
-          if (more && ok) {
-            if (j + 1 < it.n[1]) qk(t1, kd);
-            mma_commit(empty + ks);
-            if (j + 2 == blocks) mma_commit(q_empty);
+          const uint64_t kn = kd + ((j + 1) & 1 ? kHalf : 0);
+          if (j + 1 < n0 && ok) qk(t0, kn);
+          if (!(j & 1)) {
+            vs = next();
+            vd = v_desc(smem_u32(ring + vs * L::kTile));
+            if (!ok) break;
+            if (j + 2 >= steps) {  // the item's last V block
+              // In the sequence's last block the last MMA step's rows that belong to other
+              // sequences are cleared.  (The cleaner hears of every item, so that its waits
+              // are short.)
+              const int live = lk - j * kStep;
+              const bool dirty = live < kKeys && (live & 15);
+              if (n_clean > 0) wait_all(v_clean, (n_clean - 1) & 1);
+              if (lane == 0) {
+                *unclean = dirty ? vs * L::kTile + live * 128 : kNothing;
+                mbar_arrive(v_dirty);
+              }
+              ++n_clean;
+              if (dirty) wait_all(v_clean, (n_clean - 1) & 1);
+            }
           }
+          const uint64_t vn = vd + (j & 1 ? kHalf : 0);
+          const int live = lk - j * kStep;
+          if (j < n0 && ok) pv(t0, vn, live, j == 0);
+          if (j + 1 < n1 && ok) qk(t1, kn);
+          if (more && ok && (!(j & 1) || j + 2 == steps)) {  // (its second half, or the last step)
+            commit(empty + ks);
+            if (j + 2 == steps) commit(q_empty);
+          }
+          if (j < n1 && ok) pv(t1, vn, live, j == 0);
+          if ((j & 1) || !more) commit(empty + vs);
         }
       }
-      if (n_clean > 0) wait(v_clean, (n_clean - 1) & 1);
-      *unclean = kNoMore;
-      mbar_arrive(v_dirty);
-      mma_commit(drained);  // nothing of this CTA's is in flight when the TMEM goes
+      if (n_clean > 0) wait_all(v_clean, (n_clean - 1) & 1);
+      if (lane == 0) {
+        *unclean = kNoMore;
+        mbar_arrive(v_dirty);
+      }
+      commit(drained);  // nothing of this CTA's is in flight when the TMEM goes
       mbar_wait(drained, 0);
+      __syncwarp();
     }
-    __syncwarp();
-    } else if (warp == 10) {
+  } else if (warp == 10) {
     // ------------------------------------------------------------ cleaner
     // Clears the rows of a V tile's last MMA step that lie behind its sequence's end: their
     // weights are 0, but 0 times another sequence's infinity or NaN is not.
@@ -465,17 +492,15 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(v_clean);
     }
-    }
   } else {
     // ------------------------------------------------------------ softmax
-    reg_inc<kSoftmaxRegs>();
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + 2 * kKeys + t * kKeys;
+    const uint32_t ts = tmem + lanes + t * 2 * kStep, to = tmem + lanes + 4 * kStep + t * 128;
     const int tok = r / p.group, hh = r - tok * p.group;
     const float c = p.scale_log2;
-    uint32_t n_s = 0, n_o = 0;
+    uint32_t n = 0;  // steps of this tile, of all items
     for (int i = 0; ok; ++i) {
       wait(it_full + (i & 1), (i >> 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -486,27 +511,28 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const bool live = tok < it.tokens[t];
       const int seen = live ? it.pos + t * tpt + tok + 1 : 0;  // keys [0, seen) are visible
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < it.n[t]; ++j) {
-        wait(s_full + t, n_s & 1);
-        ++n_s;
+      const int steps = it.n[t];
+      for (int j = 0; j < steps; ++j, ++n) {
+        const uint32_t buf = n & 1, tb = ts + buf * kStep;
+        wait(s_full + 2 * t + buf, (n >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t s[kKeys];
-#pragma unroll
-        for (int e = 0; e < kKeys; e += 32) tmem_ld32(ts + e, s + e);
+        uint32_t s[kStep];
+        tmem_ld32(tb, s);
+        tmem_ld32(tb + 32, s + 32);
         tmem_wait_ld();
-        const int lim = seen - j * kKeys;
-        if (lim < kKeys) {
+        const int lim = seen - j * kStep;
+        if (lim < kStep) {
 #pragma unroll
-          for (int e = 0; e < kKeys; ++e)
+          for (int e = 0; e < kStep; ++e)
             if (e >= lim) s[e] = 0xff800000u;  // -inf
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < kKeys; e += 8)
+        for (int e = 0; e < kStep; e += 8)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             mx[u] = fmaxf(fmaxf(mx[u], __uint_as_float(s[e + 2 * u])), __uint_as_float(s[e + 2 * u + 1]));
@@ -520,6 +546,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             l *= alpha;
           }
           if (j > 0) {
+            wait(o_done + 2 * t + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
 #pragma unroll 1
             for (int e = 0; e < D; e += 16) {
               uint32_t o[16];
@@ -535,20 +564,17 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int e = half * 64; e < half * 64 + 64; e += 2) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, ref2);
-            const bool by_fma = e / 2 % kPairsOf >= kPairsOf - kPairsByFma;
-            const float2 w = by_fma ? exp2_fma(x) : make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
-            sum[e / 2 & 1] = add2(sum[e / 2 & 1], w);
-            s[e >> 1] = pack2<T>(w.x, w.y);
-          }
-          tmem_st32(ts + half * 32, s + half * 32);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive((half ? p_full : p_half) + t);
+        for (int e = 0; e < kStep; e += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, ref2);
+          const bool by_fma = e / 2 % kPairsOf >= kPairsOf - kPairsByFma;
+          const float2 w = by_fma ? exp2_fma(x) : make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+          sum[e / 2 & 1] = add2(sum[e / 2 & 1], w);
+          s[e >> 1] = pack2<T>(w.x, w.y);
         }
+        tmem_st32(tb, s);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full + 2 * t + buf);
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
       }
@@ -557,9 +583,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const float inv = any ? 1.f / l : 0.f;
       const size_t row = (size_t)(it.q_row + t * tpt + tok) * p.h_q + it.head * p.group + hh;
       uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * (D * 2));
-      if (it.n[t] > 0) {
-        wait(o_full + t, n_o & 1);
-        ++n_o;
+      if (steps > 0) {
+        wait(o_done + 2 * t + ((n - 1) & 1), ((n - 1) >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
