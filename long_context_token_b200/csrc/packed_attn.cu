@@ -13,9 +13,9 @@
 //               sum need no shuffle.  The reference m moves only when a logit passes it by
 //               more than 8 (log2 units); O is then rescaled in TMEM, after P(i-1) . V.
 //               P replaces S in TMEM (two 16-bit weights per column).
-//   warp 8      MMA issuer (one thread): each tile has two S buffers, and Q.K of step i + 1
-//               is issued before P.V of step i, so the softmax of a tile never waits for its
-//               own products.  (With 128-key steps S has one buffer, and the chain Q.K,
+//   warps 8, 11 MMA issuers of tile 0, 1: each tile has two S buffers, and Q.K of step i + 1
+//               is issued before P.V of step i, so the softmax of a tile need not wait for
+//               its own products.  (With 128-key steps S has one buffer, and the chain Q.K,
 //               softmax, P.V of each tile was what bounded the kernel: 1040 us for a
 //               16384-token prompt of 16 heads.)
 //   warp 9      work items and TMA loads: Q (2 x 128 rows), 128-key K and V blocks in a ring.
@@ -39,7 +39,7 @@ constexpr int kRows = 128;         // query rows per tile (the MMA's M)
 constexpr int kKeys = 128;         // keys per loaded block
 constexpr int kStep = 64;          // keys per step (the MMA's N, then its K extent)
 constexpr int kSoftmaxThreads = 256;
-constexpr int kPackedThreads = kSoftmaxThreads + 96;
+constexpr int kPackedThreads = kSoftmaxThreads + 128;
 constexpr float kMoveAt = 8.0f;    // log2 units by which a logit may pass the reference
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -65,7 +65,7 @@ struct PackedSmem {
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kItemOff = kRingOff + kStages * kTile;  // two slots
   static constexpr uint32_t kBarOff = kItemOff + 2 * 64;
-  static constexpr uint32_t kBars = 2 * kStages + 21;
+  static constexpr uint32_t kBars = 2 * kStages + 22;
   static constexpr uint32_t kSlotOff = kBarOff + kBars * 8;
   static constexpr uint32_t kBytes = kSlotOff + 16 + 1024;
   static_assert(sizeof(Item) <= 64 && kBytes <= 227 * 1024, "shared memory budget");
@@ -90,7 +90,7 @@ __host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 1
 // (2.6e-6, from the Remez exchange), n added to its exponent.  Of each kPairsOf pairs of
 // weights kPairsByFma are formed this way: the special-function units give 16 values a clock
 // and SM, the time of the block's MMAs, so they alone would bound the kernel.
-constexpr int kPairsOf = 4, kPairsByFma = 1;
+constexpr int kPairsOf = 8, kPairsByFma = 3;
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -126.f);  // (smaller ones give 2^-126: nothing next to the row's sum)
   x.y = fmaxf(x.y, -126.f);
@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint64_t* o_done = q_full + 10;
   uint64_t* it_full = q_full + 14;   // [2] item slot written
   uint64_t* it_empty = q_full + 16;  // [2] item slot read
-  uint64_t* drained = q_full + 18;
-  uint64_t* v_dirty = q_full + 19;   // rows of a V block to clear, and cleared
-  uint64_t* v_clean = q_full + 20;
+  uint64_t* v_dirty = q_full + 18;   // rows of a V block to clear, and cleared
+  uint64_t* v_clean = q_full + 19;
+  uint64_t* drained = q_full + 20;   // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   uint32_t* unclean = tmem_slot + 1;  // ring offset of the rows to clear
   auto item_slot = [&](int i) { return reinterpret_cast<Item*>(smem + L::kItemOff + 64 * (i & 1)); };
@@ -240,12 +240,11 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
+      mbar_init(empty + s, 2);  // both tiles' MMAs
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(drained, 1);
-    mbar_init(v_dirty, 1);
+    mbar_init(q_empty, 2);
+    mbar_init(v_dirty, 2);
     mbar_init(v_clean, 1);
     for (int t = 0; t < 4; ++t) {
       mbar_init(s_full + t, 1);
@@ -253,8 +252,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       mbar_init(o_done + t, 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(drained + t, 1);
       mbar_init(it_full + t, 1);
-      mbar_init(it_empty + t, kSoftmaxThreads + 1);
+      mbar_init(it_empty + t, kSoftmaxThreads + 2);
     }
     fence_mbar_init();
   }
@@ -345,135 +345,125 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         p.sync[1] = 0;
       }
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the loop and one elected thread issues: descriptors and TMEM
-    // addresses then are warp-uniform values, which the MMA takes as they are.  (From a
+  } else if (warp == 8 || warp == 11) {
+    // ------------------------------------------------------------ MMA issuers
+    // One warp per tile, so that no tile's products queue behind a wait for the other's
+    // weights.  The whole warp walks the loop and one elected thread issues: descriptors and
+    // TMEM addresses then are warp-uniform values, which the MMA takes as they are.  (From a
     // branch of a single thread each MMA cost about 115 cycles to issue, twice its run time.)
-    {
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        wait(bar, parity);
-        ok = __all_sync(0xffffffffu, ok);
-      };
-      constexpr uint32_t id_qk = idesc_f16(kRows, kStep, kBf16, false, false);
-      constexpr uint32_t id_pv = idesc_f16(kRows, D, kBf16, false, true);
-      const uint64_t qd[2] = {rows_desc(smem_u32(qs)), rows_desc(smem_u32(qs) + L::kTile)};
-      uint32_t slot = 0, q_loads = 0, n_clean = 0;
-      uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0};  // products issued of each tile, of all items
-      auto qk = [&](auto tile, uint64_t kd) {
-        constexpr int t = decltype(tile)::value;
-        const uint32_t buf = n_s[t]++ & 1;
-        const uint32_t d = tm + t * 2 * kStep + buf * kStep;
-        if (elect_one()) {
+    const int t = warp == 8 ? 0 : 1;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t td = tm + t * 2 * kStep, to = tm + 4 * kStep + t * 128;  // S buffers, O
+    constexpr uint32_t id_qk = idesc_f16(kRows, kStep, kBf16, false, false);
+    constexpr uint32_t id_pv = idesc_f16(kRows, D, kBf16, false, true);
+    const uint64_t qd = rows_desc(smem_u32(qs) + t * L::kTile);
+    uint32_t slot = 0, q_loads = 0, n_clean = 0;
+    uint32_t n_s = 0, n_p = 0;  // products issued, of all items
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      wait(bar, parity);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto qk = [&](uint64_t kd) {
+      const uint32_t buf = n_s++ & 1, d = td + buf * kStep;
+      if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ss(d, qd[t] + rows_step(kk), kd + rows_step(kk), id_qk, kk > 0 ? 1u : 0u);
-          mma_commit(s_full + 2 * t + buf);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](auto tile, uint64_t vd, int live, bool first) {
-        constexpr int t = decltype(tile)::value;
-        const uint32_t n = n_p[t]++, buf = n & 1;
-        const uint32_t o = tm + 4 * kStep + t * 128, w = tm + t * 2 * kStep + buf * kStep;
-        wait_all(p_full + 2 * t + buf, (n >> 1) & 1);
-        tc_fence_after();
-        if (!ok) return;  // (the caller's loops end with it)
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk)
-            if (kk * 16 < live)  // (MMA steps past the sequence's keys are left out)
-              mma_f16_ts(o, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
-          mma_commit(o_done + 2 * t + buf);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) mma_commit(bar);
-        __syncwarp();
-      };
-      const std::integral_constant<int, 0> t0;
-      const std::integral_constant<int, 1> t1;
-      auto next = [&]() -> uint32_t {  // the next ring slot, when it is filled
-        const uint32_t s = slot % NS;
-        wait_all(full + s, (slot / NS) & 1);
-        tc_fence_after();
-        ++slot;
-        return s;
-      };
-      constexpr uint64_t kHalf = (uint64_t)(kStep * 128 >> 4);  // rows 64.. of a K or V block
-      for (int i = 0; ok; ++i) {
-        wait_all(it_full + (i & 1), (i >> 1) & 1);
-        if (!ok) break;
-        const Item* it = item_slot(i);
-        const int n0 = __shfl_sync(0xffffffffu, it->n[0], 0), n1 = __shfl_sync(0xffffffffu, it->n[1], 0);
-        const int lk = __shfl_sync(0xffffffffu, it->lk, 0);
-        const int valid = __shfl_sync(0xffffffffu, it->valid, 0);
-        if (lane == 0) mbar_arrive(it_empty + (i & 1));
-        if (!valid) break;
-        const int steps = max(n0, n1);
-        if (steps == 0) continue;
-        wait_all(q_full, q_loads & 1);
-        ++q_loads;
-        uint32_t ks = next(), vs = 0;
-        if (!ok) break;
-        uint64_t kd = rows_desc(smem_u32(ring + ks * L::kTile)), vd = 0;
-        if (n0 > 0) qk(t0, kd);
-        if (n1 > 0) qk(t1, kd);
-        if (steps == 1) {
-          commit(empty + ks);
-          commit(q_empty);
-        }
-        for (int j = 0; j < steps && ok; ++j) {
-          // step j of P.V behind step j + 1 of Q.K
-          const bool more = j + 1 < steps;
-          if ((j & 1) && more) {
-            ks = next();
-            kd = rows_desc(smem_u32(ring + ks * L::kTile));
-          }
-          const uint64_t kn = kd + ((j + 1) & 1 ? kHalf : 0);
-          if (j + 1 < n0 && ok) qk(t0, kn);
-          if (!(j & 1)) {
-            vs = next();
-            vd = v_desc(smem_u32(ring + vs * L::kTile));
-            if (!ok) break;
-            if (j + 2 >= steps) {  // the item's last V block
-              // In the sequence's last block the last MMA step's rows that belong to other
-              // sequences are cleared.  (The cleaner hears of every item, so that its waits
-              // are short.)
-              const int live = lk - j * kStep;
-              const bool dirty = live < kKeys && (live & 15);
-              if (n_clean > 0) wait_all(v_clean, (n_clean - 1) & 1);
-              if (lane == 0) {
-                *unclean = dirty ? vs * L::kTile + live * 128 : kNothing;
-                mbar_arrive(v_dirty);
-              }
-              ++n_clean;
-              if (dirty) wait_all(v_clean, (n_clean - 1) & 1);
-            }
-          }
-          const uint64_t vn = vd + (j & 1 ? kHalf : 0);
-          const int live = lk - j * kStep;
-          if (j < n0 && ok) pv(t0, vn, live, j == 0);
-          if (j + 1 < n1 && ok) qk(t1, kn);
-          if (more && ok && (!(j & 1) || j + 2 == steps)) {  // (its second half, or the last step)
-            commit(empty + ks);
-            if (j + 2 == steps) commit(q_empty);
-          }
-          if (j < n1 && ok) pv(t1, vn, live, j == 0);
-          if ((j & 1) || !more) commit(empty + vs);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(d, qd + rows_step(kk), kd + rows_step(kk), id_qk, kk > 0 ? 1u : 0u);
+        mma_commit(s_full + 2 * t + buf);
       }
-      if (n_clean > 0) wait_all(v_clean, (n_clean - 1) & 1);
-      if (lane == 0) {
-        *unclean = kNoMore;
-        mbar_arrive(v_dirty);
-      }
-      commit(drained);  // nothing of this CTA's is in flight when the TMEM goes
-      mbar_wait(drained, 0);
       __syncwarp();
+    };
+    auto pv = [&](uint64_t vd, int live, bool first) {
+      const uint32_t n = n_p++, buf = n & 1, w = td + buf * kStep;
+      wait_all(p_full + 2 * t + buf, (n >> 1) & 1);
+      tc_fence_after();
+      if (!ok) return;  // (the caller's loops end with it)
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          if (kk * 16 < live)  // (MMA steps past the sequence's keys are left out)
+            mma_f16_ts(to, w + kk * 8, vd + v_step(kk), id_pv, kk > 0 ? 1u : first ? 0u : 1u);
+        mma_commit(o_done + 2 * t + buf);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
+    };
+    auto next = [&]() -> uint32_t {  // the next ring slot, when it is filled
+      const uint32_t s = slot % NS;
+      wait_all(full + s, (slot / NS) & 1);
+      tc_fence_after();
+      ++slot;
+      return s;
+    };
+    constexpr uint64_t kHalf = (uint64_t)(kStep * 128 >> 4);  // rows 64.. of a K or V block
+    for (int i = 0; ok; ++i) {
+      wait_all(it_full + (i & 1), (i >> 1) & 1);
+      if (!ok) break;
+      const Item* it = item_slot(i);
+      const int n = __shfl_sync(0xffffffffu, it->n[t], 0);
+      const int steps = max(n, __shfl_sync(0xffffffffu, it->n[1 - t], 0));  // the blocks to release
+      const int lk = __shfl_sync(0xffffffffu, it->lk, 0);
+      const int valid = __shfl_sync(0xffffffffu, it->valid, 0);
+      if (lane == 0) mbar_arrive(it_empty + (i & 1));
+      if (!valid) break;
+      if (steps == 0) continue;
+      wait_all(q_full, q_loads & 1);
+      ++q_loads;
+      uint32_t ks = next(), vs = 0;
+      if (!ok) break;
+      uint64_t kd = rows_desc(smem_u32(ring + ks * L::kTile)), vd = 0;
+      if (n > 0) qk(kd);
+      if (steps == 1) {
+        commit(empty + ks);
+        commit(q_empty);
+      }
+      for (int j = 0; j < steps && ok; ++j) {
+        // step j of P.V behind step j + 1 of Q.K
+        const bool more = j + 1 < steps;
+        if ((j & 1) && more) {
+          ks = next();
+          kd = rows_desc(smem_u32(ring + ks * L::kTile));
+        }
+        if (j + 1 < n && ok) qk(kd + ((j + 1) & 1 ? kHalf : 0));
+        if (more && ok && (!(j & 1) || j + 2 == steps)) {  // (its second half, or the last step)
+          commit(empty + ks);
+          if (j + 2 == steps) commit(q_empty);
+        }
+        if (!(j & 1)) {
+          vs = next();
+          vd = v_desc(smem_u32(ring + vs * L::kTile));
+          if (!ok) break;
+          if (j + 2 >= steps) {  // the item's last V block
+            // In the sequence's last block the last MMA step's rows that belong to other
+            // sequences are cleared.  (The cleaner hears of every item from both warps, so
+            // that its waits are short and neither warp can pass a phase of its answers
+            // unseen; an answer without rows is only waited for an item later.)
+            const int live = lk - j * kStep;
+            const bool dirty = live < kKeys && (live & 15);
+            if (n_clean > 0) wait_all(v_clean, (n_clean - 1) & 1);
+            if (lane == 0) {
+              if (t == 0) *unclean = dirty ? vs * L::kTile + live * 128 : kNothing;
+              mbar_arrive(v_dirty);
+            }
+            ++n_clean;
+            if (dirty) wait_all(v_clean, (n_clean - 1) & 1);
+          }
+        }
+        if (j < n && ok) pv(vd + (j & 1 ? kHalf : 0), lk - j * kStep, j == 0);
+        if ((j & 1) || !more) commit(empty + vs);
+      }
     }
+    if (n_clean > 0) wait_all(v_clean, (n_clean - 1) & 1);
+    if (lane == 0) {
+      if (t == 0) *unclean = kNoMore;
+      mbar_arrive(v_dirty);
+    }
+    commit(drained + t);  // nothing of this CTA's is in flight when the TMEM goes
+    mbar_wait(drained + t, 0);
+    __syncwarp();
   } else if (warp == 10) {
     // ------------------------------------------------------------ cleaner
     // Clears the rows of a V tile's last MMA step that lie behind its sequence's end: their
