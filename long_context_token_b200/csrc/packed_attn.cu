@@ -65,7 +65,7 @@ struct PackedSmem {
   static constexpr uint32_t kRingOff = 2 * kTile;
   static constexpr uint32_t kItemOff = kRingOff + kStages * kTile;  // two slots
   static constexpr uint32_t kBarOff = kItemOff + 2 * 64;
-  static constexpr uint32_t kBars = 2 * kStages + 22;
+  static constexpr uint32_t kBars = 2 * kStages + 30;
   static constexpr uint32_t kSlotOff = kBarOff + kBars * 8;
   static constexpr uint32_t kBytes = kSlotOff + 16 + 1024;
   static_assert(sizeof(Item) <= 64 && kBytes <= 227 * 1024, "shared memory budget");
@@ -90,7 +90,7 @@ __host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 1
 // (2.6e-6, from the Remez exchange), n added to its exponent.  Of each kPairsOf pairs of
 // weights kPairsByFma are formed this way: the special-function units give 16 values a clock
 // and SM, the time of the block's MMAs, so they alone would bound the kernel.
-constexpr int kPairsOf = 8, kPairsByFma = 3;
+constexpr int kPairsOf = 8, kPairsByFma = 1;
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -126.f);  // (smaller ones give 2^-126: nothing next to the row's sum)
   x.y = fmaxf(x.y, -126.f);
@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint64_t* v_dirty = q_full + 18;   // rows of a V block to clear, and cleared
   uint64_t* v_clean = q_full + 19;
   uint64_t* drained = q_full + 20;   // [2]
+  uint64_t* turn = q_full + 22;      // [2 tiles][4 warps] this warp may form its exponentials
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   uint32_t* unclean = tmem_slot + 1;  // ring offset of the rows to clear
   auto item_slot = [&](int i) { return reinterpret_cast<Item*>(smem + L::kItemOff + 64 * (i & 1)); };
@@ -250,6 +251,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       mbar_init(s_full + t, 1);
       mbar_init(p_full + t, kRows);
       mbar_init(o_done + t, 1);
+      mbar_init(turn + t, 1);
+      mbar_init(turn + 4 + t, 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(drained + t, 1);
@@ -491,6 +494,21 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     const int tok = r / p.group, hh = r - tok * p.group;
     const float c = p.scale_log2;
     uint32_t n = 0;  // steps of this tile, of all items
+    // Warps w and w + 4 (one of each tile) share a scheduler and its special-function unit.
+    // They form their exponentials in turn, tile 0 first: one then loads, compares and stores
+    // while the other keeps that unit busy.  Rounds count the longer tile's steps, so that both
+    // take part in each.
+    uint64_t* const my_turn = turn + warp;
+    uint64_t* const other_turn = turn + (warp ^ 4);
+    uint32_t round = 0;
+    auto take_turn = [&]() {
+      if (t == 1 || round > 0) wait(my_turn, (t == 1 ? round : round - 1) & 1);
+    };
+    auto pass_turn = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(other_turn);
+      ++round;
+    };
     for (int i = 0; ok; ++i) {
       wait(it_full + (i & 1), (i >> 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -502,6 +520,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const int seen = live ? it.pos + t * tpt + tok + 1 : 0;  // keys [0, seen) are visible
       float m = -INFINITY, l = 0.f;
       const int steps = it.n[t];
+      const int rounds = max(it.n[0], it.n[1]);
       for (int j = 0; j < steps; ++j, ++n) {
         const uint32_t buf = n & 1, tb = ts + buf * kStep;
         wait(s_full + 2 * t + buf, (n >> 1) & 1);
@@ -550,6 +569,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             }
           }
         }
+        take_turn();
         const float ref = -finite_ref(m);
         const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -561,12 +581,18 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           sum[e / 2 & 1] = add2(sum[e / 2 & 1], w);
           s[e >> 1] = pack2<T>(w.x, w.y);
         }
+        pass_turn();
         tmem_st32(tb, s);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + 2 * t + buf);
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
+      }
+      for (int j = steps; j < rounds && ok; ++j) {
+        take_turn();
+        ok = __all_sync(0xffffffffu, ok);
+        pass_turn();
       }
       if (!ok) break;
       const bool any = seen > 0;
