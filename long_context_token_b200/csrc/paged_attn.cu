@@ -100,9 +100,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {
-  const __half2 h = e4m3x2_to_half2(two & 0xffffu);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Four E4M3 codes as two float16 pairs: the low two, the high two.
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
@@ -331,17 +336,32 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     }
     const int m_tile = warp % mt, turn = warp / mt, turns = 8 / mt;
     const int c4 = lane & 3, r8 = lane >> 2;
+    // Byte offset within a tile of 16-byte chunk `c` of key `r`, in the layout TMA wrote: an
+    // even chunk added to c only flips address bits 4..6 (and, in rows of 256 bytes, adds
+    // half a load), so one offset per lane and 16 keys serves all chunks.
     const int rshift = min(p.c.page_shift, 5);  // rows of one load, log2
-    // Byte offset within a tile of 16-byte chunk `c` of key `r`, in the layout TMA wrote.
+    const uint32_t half = 128u << rshift;       // rows of 256 bytes: from a row's half to the other
     auto at = [&](int r, int c) -> uint32_t {
       if constexpr (RB == 256)
-        return ((uint32_t)(r >> rshift) << (rshift + 8)) + ((uint32_t)(c >> 3) << (rshift + 7)) +
-               (uint32_t)(r & ((1 << rshift) - 1)) * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+        return ((uint32_t)(r >> rshift) << (rshift + 8)) + (uint32_t)(r & ((1 << rshift) - 1)) * 128u +
+               (uint32_t)((c ^ (r & 7)) << 4);
       else if constexpr (RB == 128)
         return (uint32_t)r * 128u + (uint32_t)((c ^ (r & 7)) << 4);
       else
         return (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4);
     };
+    auto chunk = [&](uint32_t a, int c) -> uint32_t {  // a + even chunk c
+      if constexpr (RB == 256) return (a ^ (uint32_t)((c & 7) << 4)) + (c >= 8 ? half : 0u);
+      return a ^ (uint32_t)(c << 4);
+    };
+    // This lane's rows and first chunks in ldmatrix of K (rows by 8s, then chunks) and V (16-bit:
+    // chunks, then rows by 8s, so that the transposed fragment is V^T; codes: as K).
+    uint32_t k_at[2], v_at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k_at[i] = at(16 * i + (((lane >> 3) & 1) << 3) + (lane & 7), lane >> 4);
+      v_at[i] = kFp8 ? k_at[i] : at(16 * i + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
+    }
     uint32_t slot = 0;
     while (walk.next(p, s)) {
       // ---- queries, as the MMA's K x N operand: head r8 of each 8-head tile
@@ -408,35 +428,34 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         const int left = s.len - t * kTileKeys;  // keys of the tile (32 or more: all)
         // ---- logits: rows i * 16 + r8 (+ 8) are keys, columns heads
         float sc[2][NT][4] = {};
-        {
-          const int r = (((lane >> 3) & 1) << 3) + (lane & 7);
-          if constexpr (!kFp8) {
+        const uint32_t ka[2] = {kt + k_at[0], kt + k_at[1]}, va[2] = {vt + v_at[0], vt + v_at[1]};
+        if constexpr (!kFp8) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+          for (int k = 0; k < KS; ++k)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a[4];
+              ldsm4(chunk(ka[i], 2 * k), a);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<kBf16>(sc[i][n], a, qb[k][n][0], qb[k][n][1]);
+            }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w[4];
+              ldsm4(chunk(ka[i], k), w);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
                 uint32_t a[4];
-                ldsm4(kt + at(16 * i + r, 2 * k + (lane >> 4)), a);
+                cvt_e4m3x4(w[2 * u], a[0], a[2]);
+                cvt_e4m3x4(w[2 * u + 1], a[1], a[3]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<kBf16>(sc[i][n], a, qb[k][n][0], qb[k][n][1]);
+                for (int n = 0; n < NT; ++n)
+                  mma16816<false>(sc[i][n], a, qb[k + u][n][0], qb[k + u][n][1]);
               }
-          } else {
-#pragma unroll
-            for (int k = 0; k < KS; k += 2)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t w[4];
-                ldsm4(kt + at(16 * i + r, k + (lane >> 4)), w);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  const uint32_t a[4] = {cvt_e4m3x2(w[2 * u]), cvt_e4m3x2(w[2 * u + 1]),
-                                         cvt_e4m3x2(w[2 * u] >> 16), cvt_e4m3x2(w[2 * u + 1] >> 16)};
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-                    mma16816<false>(sc[i][n], a, qb[k + u][n][0], qb[k + u][n][1]);
-                }
-              }
-          }
+            }
         }
         // ---- logits in log2 units; keys past the sequence's end drop out
         float vs[2][2], ref_by[2][2];  // FP8: V's scales of the thread's keys and their log2
@@ -452,15 +471,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               ref_by[i][u] = fmaxf(lg2(vs[i][u]), -64.f);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& x = sc[i][n][2 * u + e];
-                x = kFp8 ? (x * kk) * f[n][e] : x * f[n][e];
-                if (key >= left) x = -INFINITY;
-              }
-            if (kFp8 && key >= left) vs[i][u] = ref_by[i][u] = 0.f;
+            for (int n = 0; n < NT; ++n) {
+              float2 x = make_float2(sc[i][n][2 * u], sc[i][n][2 * u + 1]);
+              if constexpr (kFp8) x = mul2(x, make_float2(kk, kk));
+              x = mul2(x, make_float2(f[n][0], f[n][1]));
+              sc[i][n][2 * u] = x.x;
+              sc[i][n][2 * u + 1] = x.y;
+            }
           }
+        if (left < kTileKeys) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (16 * i + 8 * u + r8 >= left) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) sc[i][n][2 * u] = sc[i][n][2 * u + 1] = -INFINITY;
+                if constexpr (kFp8) vs[i][u] = ref_by[i][u] = 0.f;
+              }
+        }
         float top[NT][2];
         bool move = false;
 #pragma unroll
@@ -525,40 +554,35 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t v0 = live(16 * i + 2 * c4), v1 = live(16 * i + 8 + 2 * c4);
+            auto cut = [&](uint32_t (&a)[4]) {
+              if constexpr (decltype(tail)::value) {
+                a[0] &= v0;
+                a[1] &= v0;
+                a[2] &= v1;
+                a[3] &= v1;
+              }
+            };
             if constexpr (!kFp8) {
-              const int r = 16 * i + ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
                 uint32_t a[4];
-                ldsm4t(vt + at(r, 2 * j + ((lane >> 3) & 1)), a);
-                if constexpr (decltype(tail)::value) {
-                  a[0] &= v0;
-                  a[1] &= v0;
-                  a[2] &= v1;
-                  a[3] &= v1;
-                }
+                ldsm4t(chunk(va[i], 2 * j), a);
+                cut(a);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma16816<kBf16>(o[j][n], a, pb[i][n][0], pb[i][n][1]);
               }
             } else {
-              const int r = 16 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
               for (int j = 0; j < KS; j += 2) {
                 uint32_t w[4];
-                ldsm4t(vt + at(r, j + (lane >> 4)), w);
+                ldsm4t(chunk(va[i], j), w);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                   // rows 0..7 are a chunk's even elements, rows 8..15 its odd ones
-                  uint32_t a[4] = {cvt_e4m3x2(__byte_perm(w[2 * u], 0, 0x4420)),
-                                   cvt_e4m3x2(__byte_perm(w[2 * u], 0, 0x4431)),
-                                   cvt_e4m3x2(__byte_perm(w[2 * u + 1], 0, 0x4420)),
-                                   cvt_e4m3x2(__byte_perm(w[2 * u + 1], 0, 0x4431))};
-                  if constexpr (decltype(tail)::value) {
-                    a[0] &= v0;
-                    a[1] &= v0;
-                    a[2] &= v1;
-                    a[3] &= v1;
-                  }
+                  uint32_t a[4];
+                  cvt_e4m3x4(__byte_perm(w[2 * u], 0, 0x3120), a[0], a[1]);
+                  cvt_e4m3x4(__byte_perm(w[2 * u + 1], 0, 0x3120), a[2], a[3]);
+                  cut(a);
 #pragma unroll
                   for (int n = 0; n < NT; ++n)
                     mma16816<false>(o[j + u][n], a, pb[i][n][0], pb[i][n][1]);
