@@ -301,7 +301,7 @@ HS2_API hs2_status hs2_kv_append(const void* k_new, const void* v_new, int n_new
  *              max_pages * page_size (taken as that) sets HS2_ERR_BAD_LENGTH.
  *   page_size  a power of two in [8, 256].
  *   max_pages * page_size < 2^31 - 64, batch <= 65535, n_kv_heads <= 1024, and
- *   batch * n_kv_heads * max_pages * page_size < 2^36 - 2^15.                             */
+ *   batch * n_kv_heads * (max_pages * page_size + 544) < 2^36 - 2^15.                        */
 typedef struct hs2_paged_kv {
   void* k;
   void* v;

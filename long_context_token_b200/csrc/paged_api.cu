@@ -31,7 +31,7 @@ static hs2_status check_paged(const hs2_paged_kv* kv) {
     return HS2_ERR_UNSUPPORTED;
   if (kv->batch > 65535 || kv->n_kv_heads > 1024 ||
       (long long)kv->max_pages * kv->page_size >= (1ll << 31) - 64 ||
-      ((long long)kv->max_pages * kv->page_size + 31) / 32 * kv->batch * kv->n_kv_heads >= (1ll << 31) - 1024)
+      ((long long)kv->max_pages * kv->page_size / 32 + 17) * kv->batch * kv->n_kv_heads >= (1ll << 31) - 1024)
     return HS2_ERR_UNSUPPORTED;
   const int elt = fp8 ? 1 : 2;
   if (!aligned16(kv->k) || !aligned16(kv->v) || !good_stride(kv->page_stride, elt) ||

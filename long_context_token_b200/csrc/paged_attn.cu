@@ -43,6 +43,10 @@ constexpr int kTileKeys = 32;
 constexpr int kConsumers = 256;
 constexpr int kProducerWarps = 4;
 constexpr int kPagedThreads = kConsumers + 32 * kProducerWarps;
+// Registers per thread: launched with 168 (65536 / 384, in eights), 64512 in all.  With two
+// 8-head tiles per warp the consumers then take 208 and the producers keep 88: 256 x 208 +
+// 128 x 88 = 64512 (the launcher checks the kernel's count).
+constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
 // Joining one partial result of one element costs this much of a tile's time in a run
 // (measured on a B200: about 65 ns per 16 heads x 128, against 0.25 us per tile of a run).
 constexpr float kJoinCost = 0.25f / 2048.f;
@@ -61,6 +65,7 @@ struct PagedSmem {
   // stages' barriers.  (A parity wait that skips a phase passes too early when the skipped
   // phase's data is late.)
   static constexpr int kStages = 128 * 1024 / (2 * kTile);
+  static constexpr int kExtra = 64 * 1024 / (2 * kTile);  // a pair's own cost, in tiles
   static constexpr uint32_t kScaleOff = kStages * 2 * kTile;
   static constexpr uint32_t kRedOff = kScaleOff + kStages * kScales;
   static constexpr uint32_t kRedFloats = 8 * 8 * NT * D;  // [8 warps][8 NT heads][D]
@@ -121,38 +126,101 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// A (sequence, K/V head) pair's part of the run, the same walk for all warps.
+// A (sequence, K/V head) pair's part of the run, the same walk for all warps.  A pair takes
+// `extra` + tiles units of the line: starting and joining it costs a CTA about as long as
+// `extra` tiles, so that a run of many short sequences gets fewer tiles.
 struct Segment {
   int b, h, len, t0, nt, tiles;  // tiles [t0, t0 + nt) of the pair's `tiles`
-  int first;                     // the line's tile at which the pair starts
+  int first;                     // the line's unit at which the pair's tiles start
 };
 
+__device__ __forceinline__ int pair_tiles(const PagedAttnParams& p, int b, bool report) {
+  return (paged_len(p.c, b, report) + kTileKeys - 1) / kTileKeys;
+}
+
+template <int kExtra>
 struct Walk {
-  int at, end;   // the rest of the run, in the line's tiles
+  int at, end;   // the rest of the run, in the line's units
   int b;         // sequence
-  int b_first;   // the line's tile at which it starts
+  int b_first;   // the line's unit at which it starts
   __device__ bool next(const PagedAttnParams& p, Segment& s) {
-    if (at >= end) return false;
-    int len = paged_len(p.c, b, false);
-    int tiles = (len + kTileKeys - 1) / kTileKeys;
-    while (at >= b_first + tiles * p.c.h_kv) {  // (also over empty sequences)
-      b_first += tiles * p.c.h_kv;
-      ++b;
-      len = paged_len(p.c, b, false);
-      tiles = (len + kTileKeys - 1) / kTileKeys;
+    while (at < end) {
+      const int len = paged_len(p.c, b, false);
+      const int tiles = (len + kTileKeys - 1) / kTileKeys, units = tiles > 0 ? tiles + kExtra : 0;
+      if (at >= b_first + units * p.c.h_kv) {  // (also over empty sequences)
+        b_first += units * p.c.h_kv;
+        ++b;
+        continue;
+      }
+      s.b = b;
+      s.len = len;
+      s.tiles = tiles;
+      const int in = at - b_first;
+      s.h = in / units;
+      const int from = in - s.h * units, to = min(units, from + (end - at));
+      s.t0 = max(from - kExtra, 0);
+      s.nt = max(to - kExtra, 0) - s.t0;
+      s.first = at - from + kExtra;
+      at += to - from;
+      if (s.nt > 0) return true;
     }
-    s.b = b;
-    s.len = len;
-    s.tiles = tiles;
-    const int in = at - b_first;
-    s.h = in / tiles;
-    s.t0 = in - s.h * tiles;
-    s.first = at - s.t0;
-    s.nt = min(tiles - s.t0, end - at);
-    at += s.nt;
-    return true;
+    return false;
   }
 };
+
+// Joins the n partial results of a pair, in the order of their CTAs: `parts` is slot 0 of the
+// first one's CTA, whose part is in slot 1 (it begins the pair); the others' are in slot 0.
+// Warp `warp` of 8 takes heads warp, warp + 8, ...; per 32 results lane c holds the weight of
+// result c, and the lanes share the head's elements, the first of which are on their way
+// before the weights are known.  (A call of its own: inlined, its registers made the main
+// loop spill.)
+template <int D, typename Q>
+__device__ __noinline__ void join_parts(const float* parts, int part_floats, int n, int group,
+                                        int warp, uint8_t* out_rows, float* lse) {
+  constexpr int E = D / 32;
+  using Piece = typename std::conditional<E == 4, float4, float2>::type;
+  const int lane = (int)lane_id();
+  auto part = [&](int c) { return parts + (size_t)(c == 0 ? 1 : 2 * c) * part_floats; };
+  for (int hr = warp; hr < group; hr += 8) {
+    float mm = -INFINITY, ll = 0.f, v[E] = {};
+    for (int from = 0; from < n; from += 32) {
+      const int k = min(n - from, 32);
+      Piece u[8];
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < k)
+            u[i] = __ldcg(reinterpret_cast<const Piece*>(part(from + c + i) + hr * D + lane * E));
+      };
+      fetch(0);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < k) ml = __ldcg(reinterpret_cast<const float2*>(part(from + lane) + group * D + 2 * hr));
+      const float top = fmaxf(mm, warp_max(ml.x));  // finite: every part holds a key
+      const float keep = ex2_ftz(mm - top), w = ex2_ftz(ml.x - top);
+      ll = fmaf(ll, keep, warp_sum(w * ml.y));
+      mm = top;
+#pragma unroll
+      for (int x = 0; x < E; ++x) v[x] *= keep;
+      for (int c = 0; c < k; c += 8) {
+        if (c > 0) fetch(c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, (c + i) & 31);
+          if (c + i < k) {
+            const float* x = reinterpret_cast<const float*>(&u[i]);
+#pragma unroll
+            for (int y = 0; y < E; ++y) v[y] = fmaf(wi, x[y], v[y]);
+          }
+        }
+      }
+    }
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(out_rows + (size_t)hr * (D * 2)) + lane * (E / 2);
+#pragma unroll
+    for (int x = 0; x < E / 2; ++x) out[x] = pack2<Q>(v[2 * x] * inv, v[2 * x + 1] * inv);
+    if (lse && lane == 0) lse[hr] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+  }
+}
 
 }  // namespace
 
@@ -191,15 +259,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   }
   griddep_wait();
 
-  // ---- the run: a prefix sum of the sequences' tiles, 256 threads of `each` sequences
+  // ---- the run: a prefix sum of the sequences' units, 256 threads of `each` sequences
   {
     const int each = (p.c.batch + 255) / 256;
     int mine = 0, longest = 0;
     const int b_lo = min((int)threadIdx.x * each, p.c.batch), b_hi = min(b_lo + each, p.c.batch);
     if (warp < 8)
       for (int b = b_lo; b < b_hi; ++b) {
-        const int n = (paged_len(p.c, b, blockIdx.x == 0) + kTileKeys - 1) / kTileKeys;
-        mine += n;
+        const int n = pair_tiles(p, b, blockIdx.x == 0);
+        mine += n > 0 ? n + L::kExtra : 0;
         longest = max(longest, n);
       }
     mine *= p.c.h_kv;
@@ -234,9 +302,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     if (warp < 8 && begin >= before && begin < before + mine) {
       int b = b_lo;
       for (;; ++b) {
-        const int n = (paged_len(p.c, b, false) + kTileKeys - 1) / kTileKeys * p.c.h_kv;
-        if (begin < before + n) break;
-        before += n;
+        const int n = pair_tiles(p, b, false), units = (n > 0 ? n + L::kExtra : 0) * p.c.h_kv;
+        if (begin < before + units) break;
+        before += units;
       }
       misc[2] = b;
       misc[3] = before;
@@ -244,7 +312,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     __syncthreads();
   }
   const int per = misc[0];
-  Walk walk;
+  Walk<L::kExtra> walk;
   walk.end = misc[1];
   walk.at = (int)min((long long)blockIdx.x * per, (long long)walk.end);
   walk.b = misc[2];
@@ -262,6 +330,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 
   if (warp >= 8) {
     // ------------------------------------------------------------ producers
+    if constexpr (NT == 2) reg_dec<kProducerRegs>();
     const int me = warp - 8;
     const int shift = p.c.page_shift, in_page = (1 << shift) - 1;
     const int rows = min(1 << shift, kTileKeys);  // rows of one load
@@ -326,6 +395,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       mbar_wait(full + (x - 1) % NS, ((x - 1) / NS) & 1);
   } else {
     // ------------------------------------------------------------ consumers
+    if constexpr (NT == 2) reg_inc<kConsumerRegs>();
     // Empty sequences have no tiles: their rows are written here, spread over the CTAs.
     for (int b = blockIdx.x; b < p.c.batch; b += gridDim.x) {
       if (paged_len(p.c, b, false) > 0) continue;
@@ -363,7 +433,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       v_at[i] = kFp8 ? k_at[i] : at(16 * i + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
     }
     uint32_t slot = 0;
-    while (walk.next(p, s)) {
+    Segment after;
+    for (bool have = walk.next(p, s), more; have; s = after, have = more) {
       // ---- queries, as the MMA's K x N operand: head r8 of each 8-head tile
       uint32_t qb[KS][NT][2];
       float f[NT][2];  // factors of the logits of heads 2 c4 and 2 c4 + 1
@@ -371,13 +442,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       for (int n = 0; n < NT; ++n) {
         const int h = m_tile * HT + n * 8 + r8;
         const uint8_t* q = p.q + (int64_t)s.b * p.q_seq + (int64_t)(s.h * p.group + h) * p.q_head;
-        const bool have = h < p.group;
+        const bool real = h < p.group;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           // FP8: a step's 16 elements in the order of the codes' registers (4 per thread)
           const int e0 = 16 * k + (kFp8 ? 4 * c4 : 2 * c4), e1 = kFp8 ? e0 + 2 : e0 + 8;
-          qb[k][n][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e0)) : 0u;
-          qb[k][n][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e1)) : 0u;
+          qb[k][n][0] = real ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e0)) : 0u;
+          qb[k][n][1] = real ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e1)) : 0u;
         }
         float g = 1.f;  // 1 / the power of two that this thread's head is multiplied by
         if constexpr (kScaleQ) {
@@ -417,6 +488,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         for (int j = 0; j < KS; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) o[j][n][u] = 0.f;
+      }
+
+      // The pair after this one, found (and its queries brought near) while this one's tiles come.
+      more = walk.next(p, after);
+      if (more && c4 < D / 64) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int h = m_tile * HT + n * 8 + r8;
+          if (h < p.group)
+            prefetch_l1(p.q + (int64_t)after.b * p.q_seq + (int64_t)(after.h * p.group + h) * p.q_head + c4 * 128);
+        }
       }
 
       for (int t = s.t0; t < s.t0 + s.nt; ++t, ++slot) {
@@ -626,42 +708,61 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const bool whole = s.nt == s.tiles;
       const size_t head0 = (size_t)s.b * p.h_q + s.h * p.group;  // row of the pair's first head
       const int part_floats = paged_part_floats(p.group, D);
-      // Partial results: slot 2c holds CTA c's first pair, slot 2c + 1 one that starts later.
-      auto part_of = [&](int c, bool later) {
-        return p.partials + (size_t)(2 * c + (later ? 1 : 0)) * part_floats;
+      // Partial results: slot 2c holds CTA c's part of a pair that began before it, slot
+      // 2c + 1 its part of one that it begins and does not end.
+      auto part_of = [&](int c, bool begins) {
+        return p.partials + (size_t)(2 * c + (begins ? 1 : 0)) * part_floats;
       };
-      float* part = part_of(blockIdx.x, s.t0 == 0 && s.first != (int)blockIdx.x * per);
+      float* part = part_of(blockIdx.x, s.t0 == 0);
       auto emit = [&](int hr, int d, float4 v, float m, float l) {  // a finished row's four elements
         const float inv = l > 0.f ? 1.f / l : 0.f;
         uint2 w = make_uint2(pack2<Q>(v.x * inv, v.y * inv), pack2<Q>(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (head0 + hr) * (D * 2) + d * 2) = w;
         if (d == 0 && p.lse) p.lse[head0 + hr] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       };
-      for (int e = threadIdx.x; e < p.group * (D / 4); e += kConsumers) {
-        const int hr = e / (D / 4), d = e % (D / 4) * 4;
-        const int swz = ((hr >> 1) & 3) << 3;
-        float mm = -INFINITY;
-        for (int x = 0; x < turns; ++x) mm = fmaxf(mm, red_ml[hr + x * mt * HT].x);
-        float ll = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = 0; x < turns; ++x) {
-          const int row = hr + x * mt * HT;
-          const float2 ml = red_ml[row];
-          const float w = ex2_ftz(ml.x - finite_ref(mm));  // 0 for a warp that saw no key
-          const float4 u = *reinterpret_cast<const float4*>(red + row * D + (d ^ swz));
-          ll = fmaf(w, ml.y, ll);
-          v.x = fmaf(w, u.x, v.x);
-          v.y = fmaf(w, u.y, v.y);
-          v.z = fmaf(w, u.z, v.z);
-          v.w = fmaf(w, u.w, v.w);
+      auto join = [&](auto warps_of_a_head) {
+        constexpr int N = decltype(warps_of_a_head)::value;
+        for (int e = threadIdx.x; e < p.group * (D / 4); e += kConsumers) {
+          const int hr = e / (D / 4), d = e % (D / 4) * 4;
+          const int swz = ((hr >> 1) & 3) << 3;
+          float2 ml[N];
+          float4 u[N];
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            const int row = hr + x * (8 / N) * HT;  // 8 / N head tiles
+            ml[x] = red_ml[row];
+            u[x] = *reinterpret_cast<const float4*>(red + row * D + (d ^ swz));
+          }
+          float mm = ml[0].x;
+#pragma unroll
+          for (int x = 1; x < N; ++x) mm = fmaxf(mm, ml[x].x);
+          float ll = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            const float w = ex2_ftz(ml[x].x - finite_ref(mm));  // 0 for a warp that saw no key
+            ll = fmaf(w, ml[x].y, ll);
+            v.x = fmaf(w, u[x].x, v.x);
+            v.y = fmaf(w, u[x].y, v.y);
+            v.z = fmaf(w, u[x].z, v.z);
+            v.w = fmaf(w, u[x].w, v.w);
+          }
+          if (whole) {
+            emit(hr, d, v, mm, ll);
+          } else {
+            *reinterpret_cast<float4*>(part + hr * D + d) = v;
+            if (d == 0) *reinterpret_cast<float2*>(part + p.group * D + 2 * hr) = make_float2(mm, ll);
+          }
         }
-        if (whole) {
-          emit(hr, d, v, mm, ll);
-        } else {
-          *reinterpret_cast<float4*>(part + hr * D + d) = v;
-          if (d == 0) *reinterpret_cast<float2*>(part + p.group * D + 2 * hr) = make_float2(mm, ll);
-        }
-      }
+      };
+      if (NT == 1 || mt == 1)
+        join(std::integral_constant<int, 8>{});
+      else if (mt == 2)
+        join(std::integral_constant<int, 4>{});
+      else if (mt == 4)
+        join(std::integral_constant<int, 2>{});
+      else
+        join(std::integral_constant<int, 1>{});
       named_bar_sync(1, kConsumers);  // the buffers are read; the partial result is written
       if (!whole) {
         const int c0 = s.first / per, n = (s.first + s.tiles - 1) / per - c0 + 1;
@@ -673,62 +774,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         }
         named_bar_sync(1, kConsumers);
         if (misc[12]) {
-          // The last CTA of the pair joins the n partial results.  Heads in batches whose
-          // n x heads weights fit the result buffer.
-          float2* ml = reinterpret_cast<float2*>(red);
-          const int batch = max(1, min(p.group, (int)(L::kRedFloats / 2) / n));
-          const bool later = s.first != c0 * per;
-          for (int h0 = 0; h0 < p.group; h0 += batch) {
-            const int heads = min(batch, p.group - h0);
-            for (int e = threadIdx.x; e < heads * n; e += kConsumers) {
-              const int c = e / heads, hr = e - c * heads;
-              ml[hr * n + c] = __ldcg(reinterpret_cast<const float2*>(
-                  part_of(c0 + c, c == 0 && later) + p.group * D + 2 * (h0 + hr)));
-            }
-            named_bar_sync(1, kConsumers);
-            for (int hr = warp; hr < heads; hr += 8) {  // a warp per head: weights in place of m
-              float mm = -INFINITY, ll = 0.f;
-              for (int c = lane; c < n; c += 32) mm = fmaxf(mm, ml[hr * n + c].x);
-              mm = warp_max(mm);
-              for (int c = lane; c < n; c += 32) {
-                const float w = ex2_ftz(ml[hr * n + c].x - finite_ref(mm));
-                ll = fmaf(w, ml[hr * n + c].y, ll);
-                ml[hr * n + c].x = w;
-              }
-              ll = warp_sum(ll);
-              __syncwarp();
-              if (lane == 0) red_ml[hr & (8 * HT - 1)] = make_float2(mm, ll);
-              __syncwarp();
-              // the head's D elements, four (two) per lane
-              const float2 t = red_ml[hr & (8 * HT - 1)];
-              constexpr int E = D / 32;
-              float v[E] = {};
-#pragma unroll 8
-              for (int c = 0; c < n; ++c) {
-                const float* q = part_of(c0 + c, c == 0 && later) + (h0 + hr) * D + lane * E;
-                const float w = ml[hr * n + c].x;
-                if constexpr (E == 4) {
-                  const float4 u = __ldcg(reinterpret_cast<const float4*>(q));
-                  v[0] = fmaf(w, u.x, v[0]);
-                  v[1] = fmaf(w, u.y, v[1]);
-                  v[2] = fmaf(w, u.z, v[2]);
-                  v[3] = fmaf(w, u.w, v[3]);
-                } else {
-                  const float2 u = __ldcg(reinterpret_cast<const float2*>(q));
-                  v[0] = fmaf(w, u.x, v[0]);
-                  v[1] = fmaf(w, u.y, v[1]);
-                }
-              }
-              const float inv = t.y > 0.f ? 1.f / t.y : 0.f;
-              uint32_t* out = reinterpret_cast<uint32_t*>(
-                  static_cast<uint8_t*>(p.out) + (head0 + h0 + hr) * (D * 2)) + lane * (E / 2);
-#pragma unroll
-              for (int u = 0; u < E / 2; ++u) out[u] = pack2<Q>(v[2 * u] * inv, v[2 * u + 1] * inv);
-              if (p.lse && lane == 0)
-                p.lse[head0 + h0 + hr] = t.y > 0.f ? (t.x + log2f(t.y)) * kLn2 : -INFINITY;
-            }
-            named_bar_sync(1, kConsumers);
-          }
+          join_parts<D, Q>(p.partials + (size_t)2 * c0 * part_floats, part_floats, n, p.group, warp,
+                           static_cast<uint8_t*>(p.out) + head0 * (D * 2),
+                           p.lse ? p.lse + head0 : nullptr);
         }
       }
     }
@@ -760,6 +808,13 @@ static cudaError_t launch_paged(const PagedAttnParams& p, cudaStream_t st) {
   auto* kernel = paged_attn_kernel<D, Q, kFp8, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
+  if (NT == 2) {
+    static const int regs = [kernel] {
+      cudaFuncAttributes a;
+      return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   const int tiles = (p.c.max_pages * page + kTileKeys - 1) / kTileKeys;
   const long long runs = ((long long)p.c.batch * p.c.h_kv * tiles + kMinTiles - 1) / kMinTiles;
   const int sms = device_sm_count() < kPagedMaxCtas ? device_sm_count() : kPagedMaxCtas;
