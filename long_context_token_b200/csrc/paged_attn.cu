@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 
   if (warp >= 8) {
     // ------------------------------------------------------------ producers
-    if constexpr (NT == 2) reg_dec<kProducerRegs>();
+    reg_dec<kProducerRegs>();
     const int me = warp - 8;
     const int shift = p.c.page_shift, in_page = (1 << shift) - 1;
     const int rows = min(1 << shift, kTileKeys);  // rows of one load
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       mbar_wait(full + (x - 1) % NS, ((x - 1) / NS) & 1);
   } else {
     // ------------------------------------------------------------ consumers
-    if constexpr (NT == 2) reg_inc<kConsumerRegs>();
+    reg_inc<kConsumerRegs>();
     // Empty sequences have no tiles: their rows are written here, spread over the CTAs.
     for (int b = blockIdx.x; b < p.c.batch; b += gridDim.x) {
       if (paged_len(p.c, b, false) > 0) continue;
@@ -433,23 +433,63 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       v_at[i] = kFp8 ? k_at[i] : at(16 * i + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
     }
     uint32_t slot = 0;
+    // The 16-byte pieces of a pair's query rows (zeros behind the group's heads).
+    const int pieces = mt * HT * (D / 8);
+    auto q_piece = [&](const Segment& g, int e) {
+      const int row = e / (D / 8), c = e % (D / 8);
+      return row < p.group ? __ldg(reinterpret_cast<const uint4*>(
+                                 p.q + (int64_t)g.b * p.q_seq +
+                                 (int64_t)(g.h * p.group + row) * p.q_head + c * 16))
+                           : make_uint4(0, 0, 0, 0);
+    };
+    auto put_piece = [&](int e, uint4 x) {
+      const int row = e / (D / 8), c = e % (D / 8);
+      reinterpret_cast<uint4*>(red)[row * (D / 8) + (c ^ (row & 7))] = x;
+    };
     Segment after;
-    for (bool have = walk.next(p, s), more; have; s = after, have = more) {
-      // ---- queries, as the MMA's K x N operand: head r8 of each 8-head tile
+    bool have = walk.next(p, s), more;
+    uint4 piece = make_uint4(0, 0, 0, 0);
+    if (have && (int)threadIdx.x < pieces) piece = q_piece(s, threadIdx.x);
+    for (; have; s = after, have = more) {
+      // ---- queries, as the MMA's K x N operand: head r8 of each 8-head tile.  The pair's rows
+      // go through the result buffer once for all warps, a row's 16-byte pieces xored with it.
+      if ((int)threadIdx.x < pieces) put_piece(threadIdx.x, piece);
+      for (int e = threadIdx.x + kConsumers; e < pieces; e += kConsumers) put_piece(e, q_piece(s, e));
+      named_bar_sync(1, kConsumers);
       uint32_t qb[KS][NT][2];
+      {
+        const uint32_t qs = smem_u32(red) + (m_tile * HT) * (D * 2);
+        auto piece_at = [&](int row, int c) -> uint32_t {
+          return qs + row * (D * 2) + ((c ^ (row & 7)) << 4);
+        };
+        if constexpr (kFp8) {  // a step's 16 elements in the order of the codes' registers
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                           : "=r"(qb[k][n][0]), "=r"(qb[k][n][1])
+                           : "r"(piece_at(n * 8 + r8, 2 * k + (c4 >> 1)) + (c4 & 1) * 8));
+        } else if constexpr (NT == 2) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t w[4];
+            ldsm4(piece_at(((lane >> 4) << 3) + (lane & 7), 2 * k + ((lane >> 3) & 1)), w);
+            qb[k][0][0] = w[0], qb[k][0][1] = w[1], qb[k][1][0] = w[2], qb[k][1][1] = w[3];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t w[4];
+            ldsm4(piece_at(lane & 7, 2 * k + (lane >> 3)), w);
+            qb[k][0][0] = w[0], qb[k][0][1] = w[1], qb[k + 1][0][0] = w[2], qb[k + 1][0][1] = w[3];
+          }
+        }
+      }
+      named_bar_sync(1, kConsumers);  // (the buffer is the results' again)
       float f[NT][2];  // factors of the logits of heads 2 c4 and 2 c4 + 1
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int h = m_tile * HT + n * 8 + r8;
-        const uint8_t* q = p.q + (int64_t)s.b * p.q_seq + (int64_t)(s.h * p.group + h) * p.q_head;
-        const bool real = h < p.group;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          // FP8: a step's 16 elements in the order of the codes' registers (4 per thread)
-          const int e0 = 16 * k + (kFp8 ? 4 * c4 : 2 * c4), e1 = kFp8 ? e0 + 2 : e0 + 8;
-          qb[k][n][0] = real ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e0)) : 0u;
-          qb[k][n][1] = real ? __ldg(reinterpret_cast<const uint32_t*>(q + 2 * e1)) : 0u;
-        }
         float g = 1.f;  // 1 / the power of two that this thread's head is multiplied by
         if constexpr (kScaleQ) {
           float top = 0.f;
@@ -490,16 +530,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           for (int u = 0; u < 4; ++u) o[j][n][u] = 0.f;
       }
 
-      // The pair after this one, found (and its queries brought near) while this one's tiles come.
+      // The pair after this one, found (and its queries fetched) while this one's tiles come.
       more = walk.next(p, after);
-      if (more && c4 < D / 64) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int h = m_tile * HT + n * 8 + r8;
-          if (h < p.group)
-            prefetch_l1(p.q + (int64_t)after.b * p.q_seq + (int64_t)(after.h * p.group + h) * p.q_head + c4 * 128);
-        }
-      }
+      if (more && (int)threadIdx.x < pieces) piece = q_piece(after, threadIdx.x);
 
       for (int t = s.t0; t < s.t0 + s.nt; ++t, ++slot) {
         if ((int)(slot & (turns - 1)) != turn) continue;
@@ -808,7 +841,7 @@ static cudaError_t launch_paged(const PagedAttnParams& p, cudaStream_t st) {
   auto* kernel = paged_attn_kernel<D, Q, kFp8, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  if (NT == 2) {
+  {
     static const int regs = [kernel] {
       cudaFuncAttributes a;
       return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;

@@ -234,10 +234,6 @@ __device__ __forceinline__ uint4 ld_global_v4_hint(const void* p, uint64_t polic
   return v;
 }
 
-__device__ __forceinline__ void prefetch_l1(const void* p) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
-}
-
 // 16-byte global -> shared copy through L2 only; `src_bytes` 0 writes zeros.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
