@@ -318,7 +318,9 @@ typedef struct hs2_paged_kv {
 
 /* Bytes of workspace for the three paged calls on this cache with h_q query heads (h_q 0:
  * hs2_paged_kv_write and hs2_paged_kv_read only); 0 if unsupported.  Zero-filled once
- * before first use, as the other workspaces; calls that share one must be ordered. */
+ * before first use, as the other workspaces; calls that share one must be ordered.  A
+ * workspace serves calls of any sizes that need no more bytes than it has (the bytes grow
+ * with h_q / n_kv_heads and head_dim only), hs2_packed_attn among them. */
 HS2_API size_t hs2_paged_workspace_bytes(const hs2_paged_kv* kv, int h_q);
 
 /* Writes new tokens' K and V rows into the pages.  The scheduler that hands out pages

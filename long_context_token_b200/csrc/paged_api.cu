@@ -52,12 +52,9 @@ static bool check_heads(int h_q, int h_kv) {
 static bool check_scale(float s) { return isfinite(s) && s > 0.f; }
 
 static size_t paged_bytes(const hs2_paged_kv* kv, int h_q) {
-  size_t n = kPagedCounterOff;
-  if (h_q) {
-    n += ((size_t)kv->batch * kv->n_kv_heads * 4 + 255) / 256 * 256;
-    n += (size_t)2 * kPagedMaxCtas * paged_part_floats(h_q / kv->n_kv_heads, kv->head_dim) * 4;
-  }
-  return n;
+  if (!h_q) return kPagedCounterOff;
+  return kPagedPartialOff +
+         (size_t)2 * kPagedMaxCtas * paged_part_floats(h_q / kv->n_kv_heads, kv->head_dim) * 4;
 }
 
 static PagedView paged_view(const hs2_paged_kv* kv, void* ws) {
@@ -178,8 +175,7 @@ hs2_status hs2_paged_attn(const void* q, int dtype, int h_q, int64_t q_seq_strid
   p.out = out;
   p.lse = lse;
   p.counters = ws_ptr<uint32_t>(workspace, kPagedCounterOff);
-  p.partials = ws_ptr<float>(workspace, kPagedCounterOff +
-                             ((size_t)kv->batch * kv->n_kv_heads * 4 + 255) / 256 * 256);
+  p.partials = ws_ptr<float>(workspace, kPagedPartialOff);
   const cudaError_t e = launch_paged_attn(p, kv->head_dim, kv->dtype, dtype, stream);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e, "paged attention launch");
 }

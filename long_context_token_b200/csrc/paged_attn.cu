@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       if (!whole) {
         const int c0 = s.first / per, n = (s.first + s.tiles - 1) / per - c0 + 1;
         if (threadIdx.x == 0) {
-          uint32_t* counter = p.counters + (size_t)s.b * p.c.h_kv + s.h;
+          uint32_t* counter = p.counters + c0;  // (a CTA begins at most one pair that it does not end)
           const bool last = atom_add_acq_rel_gpu(counter, 1u) == (uint32_t)(n - 1);
           if (last) *counter = 0;
           misc[12] = last;

@@ -59,6 +59,9 @@ def test_every_paged_call_refuses_a_bad_cache(L, change, code):
 def test_paged_workspace_sizes(L):
     kv = ctypes.byref(_kv())
     assert 4 <= L.hs2_paged_workspace_bytes(kv, 0) <= 512
+    # the same for every batch and page table: one workspace serves calls of any sizes
+    other = ctypes.byref(_kv(batch=3000, max_pages=70))
+    assert L.hs2_paged_workspace_bytes(other, 64) == L.hs2_paged_workspace_bytes(kv, 64)
     # two partial results of 8 heads x (128 + 2) floats for each of at least 148 CTAs
     assert L.hs2_paged_workspace_bytes(kv, 64) >= 2 * 148 * 8 * 130 * 4
     assert L.hs2_paged_workspace_bytes(kv, 12) == 0       # not a multiple of 8 heads
@@ -605,6 +608,57 @@ def test_on_another_stream_and_without_workspaces():
     b = hs2.packed_attn(qs, k, v, cu, stream=s)
     torch.cuda.synchronize()
     assert same(a[0], b[0].cpu()) and same(a[1], b[1].cpu())
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_of_all_shapes():
+    """Batches, groups and operators that change from call to call on the same workspace."""
+    pools = [(Pool(lens, h_kv, d, 16, kv, seed=21), h_q) for lens, h_kv, d, kv, h_q in (
+        ([9000], 1, 128, "bf16", 16), ([5, 0, 700] * 40, 4, 128, "bf16", 8),
+        ([3000, 1, 2500], 2, 64, "f16", 14), ([40000], 1, 128, "fp8", 16))]
+    ws = max((hs2.paged_workspace(cache_of(p), h) for p, h in pools), key=torch.numel)
+    g = torch.Generator().manual_seed(22)
+    x = torch.randn(300, 6, 64, generator=g).half().to(DEV)
+    cu = cu_of([100, 200]).to(DEV)
+    want = hs2.packed_attn(x[:, :4], x[:, 4:5], x[:, 5:], cu)[0]
+    for pool, h_q in pools + pools[::-1]:
+        q = torch.randn(len(pool.lens), h_q, pool.d, generator=g)
+        q = q.to(torch.float16 if pool.kv == "f16" else torch.bfloat16)
+        out, lse = hs2.paged_attn(q.to(DEV), cache_of(pool), ws)
+        check_step(pool, q, out, lse)
+        assert same(hs2.packed_attn(x[:, :4], x[:, 4:5], x[:, 5:], cu, workspace=ws)[0], want.cpu())
+    assert hs2.check_device_status(ws) == 0
+
+
+@pytest.mark.gpu
+def test_first_calls_inside_a_capture():
+    """Every operator captured in a graph without having run before in these forms."""
+    pool = Pool([50, 3], 1, 64, 8, "fp8", seed=23)
+    cache = cache_of(pool)
+    ws, pws = hs2.paged_workspace(cache, 2), hs2.packed_workspace(DEV)
+    g = torch.Generator().manual_seed(24)
+    q = torch.randn(2, 2, 64, generator=g).half()
+    x = torch.randn(53, 2, 64, generator=g).half().to(DEV)
+    qd, cu = q.to(DEV), cu_of([50, 3]).to(DEV)
+    out, lse = torch.empty_like(qd), torch.empty(2, 2, device=DEV)
+    k, v = torch.empty(53, 1, 64, device=DEV).half(), torch.empty(53, 1, 64, device=DEV).half()
+    po, pl = torch.empty_like(x), torch.empty(53, 2, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hs2.paged_kv_write(x[:2, :1], x[2:4, :1], cache, ws)  # the last row of each, again
+        hs2.paged_kv_read(cache, cu, ws, k_out=k, v_out=v)
+        hs2.paged_attn(qd, cache, ws, out=out, lse=lse)
+        hs2.packed_attn(x, k, v, cu, workspace=pws, out=po, lse=pl)
+    for b, n in enumerate(pool.lens):
+        pg, r = pool.at(b, n - 1, n)
+        pool.k[pg, :, r], pool.k_scale[pg, :, r] = quantise(x[b:b + 1, :1].cpu())
+        pool.v[pg, :, r], pool.v_scale[pg, :, r] = quantise(x[2 + b:3 + b, :1].cpu())
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        check_step(pool, q, out, lse)
+        check_prompts(x.cpu(), k.cpu(), v.cpu(), [50, 3], [50, 3], po, pl)
+    assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
 
 
 @pytest.mark.gpu
