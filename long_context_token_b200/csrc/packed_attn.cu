@@ -12,14 +12,22 @@
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns a row, so the row's maximum and
 //               sum need no shuffle.  The reference m moves only when a logit passes it by
 //               more than 8 (log2 units); O is then rescaled in TMEM, after P(i-1) . V.
-//               P replaces S in TMEM (two 16-bit weights per column).
+//               P replaces S in TMEM (two 16-bit weights per column).  The two tiles' warps
+//               on a scheduler form their exponentials in turn.
 //   warps 8, 11 MMA issuers of tile 0, 1: each tile has two S buffers, and Q.K of step i + 1
 //               is issued before P.V of step i, so the softmax of a tile need not wait for
-//               its own products.  (With 128-key steps S has one buffer, and the chain Q.K,
-//               softmax, P.V of each tile was what bounded the kernel: 1040 us for a
-//               16384-token prompt of 16 heads.)
+//               its own products.
 //   warp 9      work items and TMA loads: Q (2 x 128 rows), 128-key K and V blocks in a ring.
 //   warp 10     clears V rows of other sequences in a sequence's last block.
+//
+// What bounds it: the exponentials.  A step's 128 x 64 weights take a scheduler's warp 512
+// cycles of its special-function unit and about 740 with what cannot hide behind it, so two
+// tiles take 1480 cycles a step, in which the tensor pipe works 1090.  On a B200, one prompt
+// of 16384 tokens (16 heads, 2 K/V heads, d 128, bfloat16): 840 us, 1309 TFLOP/s, 0.79 of the
+// measured burst rate of a library product; 975 us when the call repeats until the power cap
+// lowers the clock (0.80 of the measured sustained rate).  What was measured on the way to
+// this shape, on that prompt: 128-key steps with one S buffer per tile 1040 us; the MMAs of
+// both tiles from one warp 942; without taking turns 878.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product, as the MMA needs;
 // the row sums, references and O stay in float32.
@@ -40,6 +48,7 @@ constexpr int kKeys = 128;         // keys per loaded block
 constexpr int kStep = 64;          // keys per step (the MMA's N, then its K extent)
 constexpr int kSoftmaxThreads = 256;
 constexpr int kPackedThreads = kSoftmaxThreads + 128;
+constexpr int kOneTileUpTo = 1;    // see launch_packed
 constexpr float kMoveAt = 8.0f;    // log2 units by which a logit may pass the reference
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -88,8 +97,9 @@ __host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 1
 // 2^x of two numbers at most about 2^7 on the multiply-add pipes: x = n + f with n the nearest
 // integer, 2^f by the polynomial of degree 4 with the least relative error on [-1/2, 1/2]
 // (2.6e-6, from the Remez exchange), n added to its exponent.  Of each kPairsOf pairs of
-// weights kPairsByFma are formed this way: the special-function units give 16 values a clock
-// and SM, the time of the block's MMAs, so they alone would bound the kernel.
+// weights kPairsByFma are formed this way, to relieve the special-function units: one in
+// eight (none 862 us on the prompt above, one 841, two 855, three 865, four 887: the
+// multiply-add pipes and the issue slots are not free either).
 constexpr int kPairsOf = 8, kPairsByFma = 1;
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -126.f);  // (smaller ones give 2^-126: nothing next to the row's sum)
@@ -153,7 +163,7 @@ struct ItemCursor {
   }
 
   // Item number -> item (valid 0 behind the last).  All lanes together, the same number.
-  __device__ Item find(const PackedAttnParams& p, uint32_t number, int tpt, int lane) {
+  __device__ Item find(const PackedAttnParams& p, uint32_t number, int tpt, int tiles, int lane) {
     while (number - base >= total) {
       if (b0 + 32 >= p.batch) {
         Item none = {};
@@ -161,14 +171,14 @@ struct ItemCursor {
       }
       base += total;
       b0 += 32;
-      load(p, 2 * tpt, lane);
+      load(p, tiles * tpt, lane);
     }
     const uint32_t at = number - base;
     while (at >= upto) {  // (ends: with level 0, upto is total)
       --level;
       done = have;
       above = upto;
-      have = at_least(level, 2 * tpt);
+      have = at_least(level, tiles * tpt);
       upto = __reduce_add_sync(0xffffffffu, (uint32_t)have) * (uint32_t)p.h_kv;
     }
     const uint32_t mine = (uint32_t)(have - done) * (uint32_t)p.h_kv;  // this level's
@@ -188,14 +198,14 @@ struct ItemCursor {
     Item it;
     it.valid = 1;
     it.head = (int)(nth % (uint32_t)p.h_kv);
-    const int tok0 = blk * 2 * tpt;  // within the sequence
+    const int tok0 = blk * tiles * tpt;  // within the sequence
     it.q_row = s_q0 + tok0;
     it.k_row = s_k0;
     it.lk = s_lk;
     it.pos = s_lk - s_lq + tok0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      it.tokens[t] = min(max(s_lq - tok0 - t * tpt, 0), tpt);
+      it.tokens[t] = t < tiles ? min(max(s_lq - tok0 - t * tpt, 0), tpt) : 0;
       const int last = it.pos + t * tpt + it.tokens[t] - 1;  // the tile's last token sees [0, last]
       it.n[t] = it.tokens[t] > 0 && last >= 0 ? last / kStep + 1 : 0;
     }
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   if (warp == 9) {
     // ------------------------------------------------------------ items and loads
     ItemCursor cur;
-    cur.load(p, 2 * tpt, lane);
+    cur.load(p, p.tiles * tpt, lane);
     const uint64_t keep = policy_evict_last();  // other CTAs read the same K and V
     const uint64_t once = policy_evict_first();
     uint32_t slot = 0;  // ring position (slots filled so far)
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         if (lane == 0) number = gridDim.x + atomicAdd(p.sync, 1u);
         number = __shfl_sync(0xffffffffu, number, 0);
       }
-      const Item it = cur.find(p, number, tpt, lane);
+      const Item it = cur.find(p, number, tpt, p.tiles, lane);
       wait(it_empty + (i & 1), ((i >> 1) & 1) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -502,11 +512,11 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     uint64_t* const other_turn = turn + (warp ^ 4);
     uint32_t round = 0;
     auto take_turn = [&]() {
-      if (t == 1 || round > 0) wait(my_turn, (t == 1 ? round : round - 1) & 1);
+      if (p.tiles == 2 && (t == 1 || round > 0)) wait(my_turn, (t == 1 ? round : round - 1) & 1);
     };
     auto pass_turn = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(other_turn);
+      if (p.tiles == 2 && lane == 0) mbar_arrive(other_turn);
       ++round;
     };
     for (int i = 0; ok; ++i) {
@@ -520,7 +530,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const int seen = live ? it.pos + t * tpt + tok + 1 : 0;  // keys [0, seen) are visible
       float m = -INFINITY, l = 0.f;
       const int steps = it.n[t];
-      const int rounds = max(it.n[0], it.n[1]);
+      const int rounds = p.tiles == 2 ? max(it.n[0], it.n[1]) : 0;
       for (int j = 0; j < steps; ++j, ++n) {
         const uint32_t buf = n & 1, tb = ts + buf * kStep;
         wait(s_full + 2 * t + buf, (n >> 1) & 1);
@@ -661,11 +671,18 @@ static cudaError_t launch_packed(const PackedAttnParams& p, cudaStream_t st) {
   constexpr uint32_t smem = PackedSmem<D>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // At most this many items: full blocks of every sequence, and one partial block each.
-  const long long items = ((long long)p.n_q / (2 * tpt) + p.batch) * p.h_kv;
+  // At most this many items: full blocks of every sequence, and one partial block each.  Items
+  // of one tile while they all find an SM of their own: a step of one tile takes 0.8 of the
+  // time of a step of two (2000 tokens of 8 heads: 30.6 us against 36.7), but beyond one wave
+  // two tiles per item are better (nine short prompts, 244 such items: 13.2 against 12.4;
+  // 4000 tokens of 16 heads, 504: 84.8 against 60.5).
   const int sms = device_sm_count();
+  auto items_of = [&](int tiles) { return ((long long)p.n_q / (tiles * tpt) + p.batch) * p.h_kv; };
+  PackedAttnParams q = p;
+  q.tiles = items_of(1) <= kOneTileUpTo * sms ? 1 : 2;
+  const long long items = items_of(q.tiles);
   const unsigned grid = (unsigned)(items < sms ? items : sms);
-  return launch_pdl(kernel, dim3(grid), dim3(kPackedThreads), smem, st, tq, tk, tv, p);
+  return launch_pdl(kernel, dim3(grid), dim3(kPackedThreads), smem, st, tq, tk, tv, q);
 }
 
 cudaError_t launch_packed_attn(const PackedAttnParams& p, int head_dim, int dtype, cudaStream_t s) {

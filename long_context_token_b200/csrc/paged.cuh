@@ -71,6 +71,7 @@ struct PackedAttnParams {
   const int32_t* cu_k;
   int64_t q_tok, q_head, kv_tok, kv_head;  // bytes
   int n_q, n_k, batch, h_q, h_kv, group;
+  int tiles;  // 128-row tiles per work item, 1 or 2
   float scale_log2;
   void* out;
   float* lse;

@@ -29,6 +29,12 @@
 //
 // A pair cut between CTAs leaves partial results (m, l, o) in the workspace; the CTA that
 // arrives last joins them in CTA order, so the result does not depend on timing.
+//
+// What bounds it: memory while the runs last (7 TB/s of rows in the steady state), and 6 to
+// 10 us of latencies around them: the run and the first pages (3 us), the join within the CTA,
+// the arrival and the join of the parts (4 us).  On a B200, 8 x 131072 bfloat16 keys of one
+// K/V head under 16 query heads: 90 us, 5.94 TB/s, 0.91 of the measured copy rate; 64
+// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 97 us, 5.2 TB/s, 0.79.
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tc_common.cuh"

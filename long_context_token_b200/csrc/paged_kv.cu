@@ -8,12 +8,15 @@
 // row of a (token, head) pair at a time and loads the next pair before it converts and
 // stores this one; an E4M3 row is a whole number of 16-byte pieces.
 //
-// A division per element (the library's takes some 10 instructions, most of them branches
-// here) would bound the kernel, so the quotients of a row, which share their divisor, are
-// formed from its reciprocal and corrected twice by their remainder: Markstein's method
-// ("Computation of elementary functions on the IBM RISC System/6000 processor", 1990), which
-// gives the correctly rounded quotient from a quotient within one unit in the last place and
-// the correctly rounded reciprocal.
+// A division per element bound the writing of FP8 rows (145 us where it now takes 82), so the
+// quotients of a row, which share their divisor, are formed from its reciprocal and corrected
+// twice by their remainder: Markstein's method ("Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990), which gives the correctly rounded quotient from one
+// within a unit in the last place and the correctly rounded reciprocal.
+//
+// What bounds them: memory, and about 5 us of look-ups and tail.  On a B200: 65K tokens of 8
+// heads (d 128, bfloat16) into an FP8 cache 82 us, 4.9 TB/s, 0.75 of the measured copy rate;
+// 67K tokens back 75 us, 5.5 TB/s, 0.84; a single token 2.2 us.
 #include "paged.cuh"
 
 namespace hs2 {

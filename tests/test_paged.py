@@ -480,17 +480,52 @@ def test_prompt_prefixes(d, dtype, lq, lk):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_prompt_large_logits(dtype):
-    run_prompts([400, 150], [400, 150], 4, 2, 128, dtype, scale=3.0)
+@pytest.mark.parametrize("d,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("h_q,h_kv,lq,lk", [
+    # enough work for two tiles per work item: both full, the second short, empty or ahead
+    (16, 16, [513, 3, 300, 256, 129, 128, 127, 1], None),
+    (32, 8, [65, 700, 64, 0, 1, 33], None),
+    (14, 2, [1300, 36, 18, 19], None),          # 18 tokens x 7 heads a tile
+    (40, 8, [300, 50, 500], [900, 20, 700]),    # prefixes, and queries that see nothing
+    (32, 16, [1] * 30, list(range(1, 600, 20))),
+    (16, 16, [200, 64, 320], [200, 0, 320]),
+])
+def test_prompt_two_tiles(d, dtype, h_q, h_kv, lq, lk):
+    run_prompts(lq, lk or lq, h_q, h_kv, d, dtype, pad_q=3, pad_k=0 if lk is None else 4,
+                fused=lk is None)
 
 
 @pytest.mark.gpu
-def test_prompt_garbage_stays_in_its_sequence():
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("h_q,h_kv", [(4, 2), (16, 16)])
+def test_prompt_large_logits(dtype, h_q, h_kv):
+    run_prompts([400, 150, 300], [400, 150, 300], h_q, h_kv, 128, dtype, scale=3.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h_q,h_kv", [(2, 1), (16, 16)])
+def test_prompt_rising_logits(h_q, h_kv):
+    """Keys whose logits rise along the prompt: the softmax reference moves in every step and
+    the outputs so far are rescaled each time."""
+    n, d = 700, 64
+    g = torch.Generator().manual_seed(25)
+    q = (torch.randn(n, h_q, d, generator=g) * 0.1 + 1).half()
+    k = torch.randn(n, h_kv, d, generator=g) * 0.1 + torch.linspace(-3, 6, n)[:, None, None]
+    v = torch.randn(n, h_kv, d, generator=g).half()
+    k = k.half()
+    ws = hs2.packed_workspace(DEV)
+    out, lse = hs2.packed_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu_of([n]).to(DEV), workspace=ws)
+    assert hs2.check_device_status(ws) == 0
+    check_prompts(q, k, v, [n], [n], out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [(4, 2, 2), (40, 40, 40)])  # one and two tiles per work item
+def test_prompt_garbage_stays_in_its_sequence(heads):
     """Infinities and NaN in one sequence's rows, and in rows no sequence owns, reach no other."""
     lens = [100, 61, 130]
     g = torch.Generator().manual_seed(14)
-    q, k, v = (torch.randn(300, h, 64, generator=g).to(torch.bfloat16).to(DEV) for h in (4, 2, 2))
+    q, k, v = (torch.randn(300, h, 64, generator=g).to(torch.bfloat16).to(DEV) for h in heads)
     cu = cu_of(lens).to(DEV)
     ws = hs2.packed_workspace(DEV)
     clean, _ = hs2.packed_attn(q, k, v, cu, workspace=ws)
