@@ -10,13 +10,13 @@
 
 namespace hs2 {
 
-// Workspace of the paged calls: the status word, an arrival counter per CTA of paged_attn
-// (of the pair that it begins and does not end; 0 between calls), then the CTAs' partial
-// results, two each.  The places do not depend on the sizes of a call, so one workspace
+// Workspace of the paged calls: the status word, two arrival counters per CTA of paged_attn
+// (of the group of CTAs that it begins, and of the groups of the pair that it begins; 0
+// between calls), then the CTAs' partial results, two each.  The places do not depend on the sizes of a call, so one workspace
 // serves calls of different shapes.
 constexpr int kPagedMaxCtas = kSmCountBound;
 constexpr size_t kPagedCounterOff = 256;
-constexpr size_t kPagedPartialOff = kPagedCounterOff + (kPagedMaxCtas * 4 + 255) / 256 * 256;
+constexpr size_t kPagedPartialOff = kPagedCounterOff + (2 * kPagedMaxCtas * 4 + 255) / 256 * 256;
 // Floats of one partial result: o [group][head_dim], then (m, l) of each head.
 __host__ __device__ constexpr int paged_part_floats(int group, int head_dim) {
   return (group * (head_dim + 2) + 3) / 4 * 4;

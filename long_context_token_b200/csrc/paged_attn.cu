@@ -27,14 +27,16 @@
 // query against codes is brought to float16 by a power of two per head, exactly down to
 // 2^-29 of its largest element.
 //
-// A pair cut between CTAs leaves partial results (m, l, o) in the workspace; the CTA that
-// arrives last joins them in CTA order, so the result does not depend on timing.
+// A pair cut between CTAs leaves partial results (m, l, o) in the workspace; the CTAs that
+// arrive last join them, in CTA order and fixed groups, so the result does not depend on timing.
 //
 // What bounds it: memory while the runs last (7 TB/s of rows in the steady state), and 6 to
 // 10 us of latencies around them: the run and the first pages (3 us), the join within the CTA,
 // the arrival and the join of the parts (4 us).  On a B200, 8 x 131072 bfloat16 keys of one
 // K/V head under 16 query heads: 90 us, 5.94 TB/s, 0.91 of the measured copy rate; 64
-// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 97 us, 5.2 TB/s, 0.79.
+// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 97 us, 5.2 TB/s, 0.79.  Groups of 64
+// and more heads are bound by the products and conversions, which every 16 heads repeat: one
+// sequence of 131072 FP8 keys under 64 heads 55 us.
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tc_common.cuh"
@@ -53,9 +55,7 @@ constexpr int kPagedThreads = kConsumers + 32 * kProducerWarps;
 // 8-head tiles per warp the consumers then take 208 and the producers keep 88: 256 x 208 +
 // 128 x 88 = 64512 (the launcher checks the kernel's count).
 constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
-// Joining one partial result of one element costs this much of a tile's time in a run
-// (measured on a B200: about 65 ns per 16 heads x 128, against 0.25 us per tile of a run).
-constexpr float kJoinCost = 0.25f / 2048.f;
+constexpr int kJoinAtOnce = 16;  // partial results that one CTA joins without groups
 constexpr int kMinTiles = 8;  // a run is at least a tile for each warp
 constexpr float kMoveAt = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -174,19 +174,23 @@ struct Walk {
   }
 };
 
-// Joins the n partial results of a pair, in the order of their CTAs: `parts` is slot 0 of the
-// first one's CTA, whose part is in slot 1 (it begins the pair); the others' are in slot 0.
-// Warp `warp` of 8 takes heads warp, warp + 8, ...; per 32 results lane c holds the weight of
-// result c, and the lanes share the head's elements, the first of which are on their way
+// Joins n partial results, in the order of their CTAs: part i is in slot 0 of CTA
+// first + i * step, part 0 in slot 1 if that CTA begins the pair.  The result becomes the
+// finished rows (out_rows, lse) or, with out_rows null, takes the place of part 0.
+// Warp `warp` of 8 takes heads warp, warp + 8, ...; per 32 parts lane c holds the weight of
+// part c, and the lanes share the head's elements, the first of which are on their way
 // before the weights are known.  (A call of its own: inlined, its registers made the main
 // loop spill.)
 template <int D, typename Q>
-__device__ __noinline__ void join_parts(const float* parts, int part_floats, int n, int group,
-                                        int warp, uint8_t* out_rows, float* lse) {
+__device__ __noinline__ void join_parts(float* partials, int part_floats, int first, int step,
+                                        bool begins, int n, int group, int warp,
+                                        uint8_t* out_rows, float* lse) {
   constexpr int E = D / 32;
   using Piece = typename std::conditional<E == 4, float4, float2>::type;
   const int lane = (int)lane_id();
-  auto part = [&](int c) { return parts + (size_t)(c == 0 ? 1 : 2 * c) * part_floats; };
+  auto part = [&](int i) {
+    return partials + (size_t)(2 * (first + i * step) + (i == 0 && begins ? 1 : 0)) * part_floats;
+  };
   for (int hr = warp; hr < group; hr += 8) {
     float mm = -INFINITY, ll = 0.f, v[E] = {};
     for (int from = 0; from < n; from += 32) {
@@ -220,11 +224,19 @@ __device__ __noinline__ void join_parts(const float* parts, int part_floats, int
         }
       }
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(out_rows + (size_t)hr * (D * 2)) + lane * (E / 2);
+    if (out_rows) {
+      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      uint32_t* out = reinterpret_cast<uint32_t*>(out_rows + (size_t)hr * (D * 2)) + lane * (E / 2);
 #pragma unroll
-    for (int x = 0; x < E / 2; ++x) out[x] = pack2<Q>(v[2 * x] * inv, v[2 * x + 1] * inv);
-    if (lse && lane == 0) lse[hr] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+      for (int x = 0; x < E / 2; ++x) out[x] = pack2<Q>(v[2 * x] * inv, v[2 * x + 1] * inv);
+      if (lse && lane == 0) lse[hr] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    } else {
+      // (this warp has read all of the head's parts)
+      float* to = part(0);
+#pragma unroll
+      for (int x = 0; x < E; ++x) to[hr * D + lane * E + x] = v[x];
+      if (lane == 0) *reinterpret_cast<float2*>(to + group * D + 2 * hr) = make_float2(mm, ll);
+    }
   }
 }
 
@@ -268,13 +280,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   // ---- the run: a prefix sum of the sequences' units, 256 threads of `each` sequences
   {
     const int each = (p.c.batch + 255) / 256;
-    int mine = 0, longest = 0;
+    int mine = 0;
     const int b_lo = min((int)threadIdx.x * each, p.c.batch), b_hi = min(b_lo + each, p.c.batch);
     if (warp < 8)
       for (int b = b_lo; b < b_hi; ++b) {
         const int n = pair_tiles(p, b, blockIdx.x == 0);
         mine += n > 0 ? n + L::kExtra : 0;
-        longest = max(longest, n);
       }
     mine *= p.c.h_kv;
     int incl = mine;
@@ -283,23 +294,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    longest = __reduce_max_sync(0xffffffffu, longest);
     if (warp < 8 && lane == 31) misc[4 + warp] = incl;
     if (threadIdx.x == 0) misc[2] = misc[3] = 0;
-    // (the warps' longest sequences meet in the not yet used result buffer)
-    if (warp < 8 && lane == 0) reinterpret_cast<int*>(red)[warp] = longest;
     __syncthreads();
     int before = incl - mine, total = 0;
     for (int w = 0; w < 8; ++w) {
       if (w < warp) before += misc[4 + w];
       total += misc[4 + w];
-      longest = max(longest, reinterpret_cast<int*>(red)[w]);
     }
-    // Equal runs; but a pair cut into n runs costs the last of them n partial results to
-    // join, so short lines are cut less: about as long a run as joining its pair takes.
-    int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int cut = (int)sqrtf((float)longest * (float)(p.group * D) * kJoinCost);
-    per = max(max(per, cut), kMinTiles);
+    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinTiles);
     const int begin = (int)min((long long)blockIdx.x * per, (long long)total);
     if (threadIdx.x == 0) {
       misc[0] = per;
@@ -804,19 +807,41 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         join(std::integral_constant<int, 1>{});
       named_bar_sync(1, kConsumers);  // the buffers are read; the partial result is written
       if (!whole) {
+        // The n parts of the pair are joined by the CTA that arrives last; with more than
+        // kJoinAtOnce of them first in groups of r neighbours, each by the last CTA of the
+        // group, and then the groups' results by the last of those.  (One CTA alone took 15 us
+        // longer over the 148 parts of a sequence of 131072 keys under 16 heads, 64 us longer
+        // under 64.)
         const int c0 = s.first / per, n = (s.first + s.tiles - 1) / per - c0 + 1;
-        if (threadIdx.x == 0) {
-          uint32_t* counter = p.counters + c0;  // (a CTA begins at most one pair that it does not end)
-          const bool last = atom_add_acq_rel_gpu(counter, 1u) == (uint32_t)(n - 1);
-          if (last) *counter = 0;
-          misc[12] = last;
+        const int r = n <= kJoinAtOnce ? n : (int)ceilf(sqrtf((float)n)), groups = (n + r - 1) / r;
+        const int g = ((int)blockIdx.x - c0) / r, g0 = c0 + g * r, members = min(r, n - g * r);
+        // Whether this CTA is the last of `of` to count up `counter`.
+        auto last_of = [&](uint32_t* counter, int of) {
+          if (threadIdx.x == 0) {
+            const bool last = atom_add_acq_rel_gpu(counter, 1u) == (uint32_t)(of - 1);
+            if (last) *counter = 0;
+            misc[12] = last;
+          }
+          named_bar_sync(1, kConsumers);
+          const bool last = misc[12];
+          named_bar_sync(1, kConsumers);  // (misc is free again, all writes before are done)
+          return last;
+        };
+        uint8_t* out_rows = static_cast<uint8_t*>(p.out) + head0 * (D * 2);
+        float* lse_rows = p.lse ? p.lse + head0 : nullptr;
+        // (Counters by CTA: one that begins a group of two or more neither begins nor ends
+        // another pair's group, and one CTA begins at most one pair that it does not end.)
+        bool last = members == 1 || last_of(p.counters + g0, members);
+        if (last && groups > 1) {
+          if (members > 1) {
+            join_parts<D, Q>(p.partials, part_floats, g0, 1, g == 0, members, p.group, warp, nullptr, nullptr);
+            named_bar_sync(1, kConsumers);
+          }
+          last = last_of(p.counters + kPagedMaxCtas + c0, groups);
         }
-        named_bar_sync(1, kConsumers);
-        if (misc[12]) {
-          join_parts<D, Q>(p.partials + (size_t)2 * c0 * part_floats, part_floats, n, p.group, warp,
-                           static_cast<uint8_t*>(p.out) + head0 * (D * 2),
-                           p.lse ? p.lse + head0 : nullptr);
-        }
+        if (last)
+          join_parts<D, Q>(p.partials, part_floats, c0, groups > 1 ? r : 1, true, groups > 1 ? groups : n,
+                           p.group, warp, out_rows, lse_rows);
       }
     }
     __threadfence();  // the results are visible before the next kernel may start
