@@ -646,6 +646,74 @@ def test_on_another_stream_and_without_workspaces():
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits_in_the_pages():
+    """A pool of 4.7 GB per tensor whose last pages are in use: every operator on them."""
+    n, page, lens = 290000, 64, [130, 64, 1]
+    pool = Pool(lens, 1, 128, page, "bf16", seed=26)
+    small = pool.k, pool.v, pool.pages.clone()
+    far = torch.tensor([0, n - 1, 140000, n - 7, 200000, 131071, 131072, n - 2], dtype=torch.int32)
+    k, v = (torch.empty(n, 1, page, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for at in range(pool.num_pages):
+        k[far[at]], v[far[at]] = small[0][at].to(DEV), small[1][at].to(DEV)
+    used = pool.pages >= 0
+    pages = torch.where(used, far[pool.pages.clamp(min=0).long()], pool.pages)
+    cache = hs2.PagedCache(k, v, pages.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    ws = hs2.paged_workspace(cache, 4)
+    q = torch.randn(3, 4, 128, generator=torch.Generator().manual_seed(27)).to(torch.bfloat16)
+    out, lse = hs2.paged_attn(q.to(DEV), cache, ws)
+    check_step(pool, q, out, lse)
+    rows = hs2.paged_kv_read(cache, cu_of(lens).to(DEV), ws)
+    for i, got in enumerate(rows):
+        assert same(got, torch.cat([pool.rows(b, 0, m)[i] for b, m in enumerate(lens)]).to(torch.bfloat16))
+    x = torch.randn(3, 1, 128, device=DEV).to(torch.bfloat16)
+    hs2.paged_kv_write(x, x + 1, cache, ws)  # the last row of each
+    again = hs2.paged_kv_read(cache, cu_of([1] * 3).to(DEV), ws,
+                              start=cache.lens - 1, n_tokens=3)
+    assert same(again[0], x.cpu()) and same(again[1], (x + 1).cpu())
+    assert hs2.check_device_status(ws) == 0
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits_in_the_prompts():
+    """150000 tokens of 128 heads of 128: 2.4e9 elements of q and out."""
+    h, d, n, m = 128, 128, 150000, 50
+    q = torch.empty(n, h, d, dtype=torch.float16, device=DEV)
+    for a in range(0, n, 10000):
+        q[a:a + 10000].normal_()
+    k, v = (torch.randn(n, 1, d, device=DEV).half() for _ in range(2))
+    cu = torch.arange(0, n + 1, m, dtype=torch.int32, device=DEV)
+    ws = hs2.packed_workspace(DEV)
+    out, lse = hs2.packed_attn(q, k, v, cu, workspace=ws)
+    assert hs2.check_device_status(ws) == 0
+    for a in (0, 131050, n - m):  # 131072 tokens of 128 x 128: 2^31 elements
+        s = slice(a, a + m)
+        check_prompts(q[s, ::37].cpu(), k[s].cpu(), v[s].cpu(), [m], [m], out[s, ::37], lse[s, ::37])
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Decode and prompts on two streams, each with its own workspace, over and over."""
+    pool = Pool([3000, 1, 777, 2000], 4, 128, 32, "fp8", seed=28)
+    cache, ws, q, out, lse = run_step(pool, 16, "bf16")
+    g = torch.Generator().manual_seed(29)
+    x = torch.randn(1500, 24, 64, generator=g).half().to(DEV)
+    cu, pws = cu_of([700, 0, 800]).to(DEV), hs2.packed_workspace(DEV)
+    args = (x[:, :16], x[:, 16:20], x[:, 20:], cu)
+    want = hs2.packed_attn(*args, workspace=pws)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(30):
+        got.append(hs2.paged_attn(q, cache, ws, stream=streams[0])
+                   + hs2.packed_attn(*args, workspace=pws, stream=streams[1]))
+    torch.cuda.synchronize()
+    for o, z, po, pz in got:
+        assert same(o, out.cpu()) and same(z, lse.cpu())
+        assert same(po, want[0].cpu()) and same(pz, want[1].cpu())
+    assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
+
+
+@pytest.mark.gpu
 def test_one_workspace_for_calls_of_all_shapes():
     """Batches, groups and operators that change from call to call on the same workspace."""
     pools = [(Pool(lens, h_kv, d, 16, kv, seed=21), h_q) for lens, h_kv, d, kv, h_q in (
