@@ -872,12 +872,13 @@ static cudaError_t launch_paged(const PagedAttnParams& p, cudaStream_t st) {
   auto* kernel = paged_attn_kernel<D, Q, kFp8, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  {
-    static const int regs = [kernel] {
-      cudaFuncAttributes a;
-      return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  static bool checked = false;  // (a race only checks twice)
+  if (!checked) {
+    cudaFuncAttributes a;
+    const cudaError_t q = cudaFuncGetAttributes(&a, kernel);
+    if (q != cudaSuccess) return q;
+    if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    checked = true;
   }
   const int tiles = (p.c.max_pages * page + kTileKeys - 1) / kTileKeys;
   const long long runs = ((long long)p.c.batch * p.c.h_kv * tiles + kMinTiles - 1) / kMinTiles;
