@@ -467,10 +467,10 @@ def _new(stream, make, *shape, **kw) -> torch.Tensor:
         return make(*shape, **kw)
 
 
-def _check_on(index: int, **tensors) -> None:
-    for name, t in tensors.items():
+def _check_on(index: int, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
         if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} must be on cuda:{index}, like the other tensors")
+            raise ValueError(f"every tensor of a call must be on the same device (cuda:{index})")
 
 
 def _check_int32(name: str, t: torch.Tensor, shape: Tuple[int, ...]) -> None:
@@ -486,17 +486,19 @@ def _check_ws(ws: torch.Tensor) -> None:
 def _row_strides(name: str, t: torch.Tensor) -> Tuple[int, ...]:
     """Strides of all axes but the last, which must be contiguous.  Axes of one element get
     the dense stride: theirs is never used and may be anything."""
-    *strides, last = t.stride()
-    if last != 1 and t.shape[-1] > 1:
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    shape = t.shape
+    strides = strides[:-1]
     if 1 in shape:
+        strides = list(strides)
         dense = shape[-1]
         for i in range(len(strides) - 1, -1, -1):
             if shape[i] <= 1:
                 strides[i] = dense
             dense *= shape[i]
-    return tuple(strides)
+        strides = tuple(strides)
+    return strides
 
 
 class PagedCache:
@@ -517,7 +519,7 @@ class PagedCache:
         if not k.is_cuda:
             raise ValueError("k must be a CUDA tensor")
         self.index = k.get_device()
-        _check_on(self.index, v=v, pages=pages, lens=lens, k_scale=k_scale, v_scale=v_scale)
+        _check_on(self.index, v, pages, lens, k_scale, v_scale)
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be [num_pages, h_kv, page_size, d] of one type")
         if not fp8 and k.dtype not in _FLOAT16S:
@@ -568,17 +570,18 @@ def paged_workspace(cache: PagedCache, h_q: int = 0) -> torch.Tensor:
 def _check_rows(k_name: str, v_name: str, k: torch.Tensor, v: torch.Tensor, cache: PagedCache,
                 ws: torch.Tensor):
     """Packed rows of a paged cache (and the workspace): their type code and strides."""
-    if k.dim() != 3 or k.shape[1:] != (cache.h_kv, cache.head_dim) or v.shape != k.shape \
-            or v.dtype != k.dtype or k.dtype not in cache.row_dtypes:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape[1] != cache.h_kv or shape[2] != cache.head_dim \
+            or v.shape != shape or v.dtype != dtype or dtype not in cache.row_dtypes:
         raise ValueError(f"{k_name} and {v_name} must be [T, {cache.h_kv}, {cache.head_dim}] of "
                          f"one type of {cache.row_dtypes}")
     strides = _row_strides(k_name, k)
-    if strides != (_row_strides(v_name, v) if v.stride() != k.stride() else strides):
+    if v.stride() != k.stride() and _row_strides(v_name, v) != strides:
         raise ValueError(f"{k_name} and {v_name} must have the same strides")
     if not k.get_device() == v.get_device() == ws.get_device() == cache.index:
         raise ValueError(f"{k_name}, {v_name} and the workspace must be on the cache's device")
     _check_ws(ws)
-    return _FLOAT16S[k.dtype], strides
+    return _FLOAT16S[dtype], strides
 
 
 def paged_kv_write(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedCache,
@@ -591,7 +594,7 @@ def paged_kv_write(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedCache,
     dtype, strides = _check_rows("k_new", "v_new", k_new, v_new, cache, workspace)
     if cu_new is not None:
         _check_int32("cu_new", cu_new, (cache.batch + 1,))
-        _check_on(cache.index, cu_new=cu_new)
+        _check_on(cache.index, cu_new)
     _launch("hs2_paged_kv_write", cache.index, stream, k_new.data_ptr(), v_new.data_ptr(),
             dtype, *strides, k_new.shape[0], _ptr(cu_new), cache.ref(), workspace.data_ptr(),
             workspace.numel())
@@ -609,7 +612,7 @@ def paged_kv_read(cache: PagedCache, cu: torch.Tensor, workspace: torch.Tensor,
     _check_int32("cu", cu, (cache.batch + 1,))
     if start is not None:
         _check_int32("start", start, (cache.batch,))
-    _check_on(cache.index, cu=cu, start=start)
+    _check_on(cache.index, cu, start)
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     if k_out is None:
@@ -647,7 +650,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, workspace: Optional[torch.Ten
     strides = _row_strides("q", q)
     _check_out("out", out, q.dtype, shape)
     _check_out("lse", lse, torch.float32, shape[:2])
-    _check_on(cache.index, q=q, out=out, lse=lse, workspace=workspace)
+    _check_on(cache.index, q, out, lse, workspace)
     if workspace is None:
         n = lib().hs2_paged_workspace_bytes(cache.ref(), h_q)
         if n == 0:
@@ -695,11 +698,11 @@ def packed_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     shape, index = q.shape, q.get_device()
     tq, h_q, d = shape
     q_strides, kv_strides = _row_strides("q", q), _row_strides("k", k)
-    if kv_strides != (_row_strides("v", v) if v.stride() != k.stride() else kv_strides):
+    if v.stride() != k.stride() and _row_strides("v", v) != kv_strides:
         raise ValueError("k and v must have the same strides")
     _check_out("out", out, q.dtype, shape)
     _check_out("lse", lse, torch.float32, shape[:2])
-    _check_on(index, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, workspace=workspace)
+    _check_on(index, k, v, cu_q, cu_k, out, lse, workspace)
     if workspace is None:
         workspace = _new(stream, packed_workspace, q.device)
     _check_ws(workspace)
