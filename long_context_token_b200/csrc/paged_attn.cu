@@ -36,7 +36,7 @@
 // K/V head under 16 query heads: 90 us, 5.94 TB/s, 0.91 of the measured copy rate; 64
 // sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 97 us, 5.2 TB/s, 0.79.  Groups of 64
 // and more heads are bound by the products and conversions, which every 16 heads repeat: one
-// sequence of 131072 FP8 keys under 64 heads 55 us.
+// sequence of 1048576 FP8 keys under 64 heads takes 190 us, 4.5 times its bytes' time.
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tc_common.cuh"
@@ -55,7 +55,7 @@ constexpr int kPagedThreads = kConsumers + 32 * kProducerWarps;
 // 8-head tiles per warp the consumers then take 208 and the producers keep 88: 256 x 208 +
 // 128 x 88 = 64512 (the launcher checks the kernel's count).
 constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
-constexpr int kJoinAtOnce = 16;  // partial results that one CTA joins without groups
+constexpr int kJoinAtOnce = 512;  // rows (heads x partial results) that one CTA joins alone
 constexpr int kMinTiles = 8;  // a run is at least a tile for each warp
 constexpr float kMoveAt = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -808,12 +808,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       named_bar_sync(1, kConsumers);  // the buffers are read; the partial result is written
       if (!whole) {
         // The n parts of the pair are joined by the CTA that arrives last; with more than
-        // kJoinAtOnce of them first in groups of r neighbours, each by the last CTA of the
+        // kJoinAtOnce rows in them first in groups of r neighbours, each by the last CTA of the
         // group, and then the groups' results by the last of those.  (One CTA alone took 15 us
         // longer over the 148 parts of a sequence of 131072 keys under 16 heads, 64 us longer
         // under 64.)
         const int c0 = s.first / per, n = (s.first + s.tiles - 1) / per - c0 + 1;
-        const int r = n <= kJoinAtOnce ? n : (int)ceilf(sqrtf((float)n)), groups = (n + r - 1) / r;
+        const int r = n * p.group <= kJoinAtOnce ? n : (int)ceilf(sqrtf((float)n)), groups = (n + r - 1) / r;
         const int g = ((int)blockIdx.x - c0) / r, g0 = c0 + g * r, members = min(r, n - g * r);
         // Whether this CTA is the last of `of` to count up `counter`.
         auto last_of = [&](uint32_t* counter, int of) {
