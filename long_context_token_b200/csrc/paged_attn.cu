@@ -71,7 +71,10 @@ struct PagedSmem {
   // stages' barriers.  (A parity wait that skips a phase passes too early when the skipped
   // phase's data is late.)
   static constexpr int kStages = 128 * 1024 / (2 * kTile);
-  static constexpr int kExtra = 64 * 1024 / (2 * kTile);  // a pair's own cost, in tiles
+  // A pair's own cost, in tiles: 128 KB of rows, at most 16 tiles (128 sequences of 1 .. 600
+  // bfloat16 keys, 64 heads on 8, d 128: 40.5 us with 8 tiles, 53.8 with 4, 59.0 with 2; of
+  // 1 .. 3000 FP8 keys, 32 on 4, d 64: 42.5 with 16, 46.0 with 32).
+  static constexpr int kExtra = 128 * 1024 / (2 * kTile) > 16 ? 16 : 128 * 1024 / (2 * kTile);
   static constexpr uint32_t kScaleOff = kStages * 2 * kTile;
   static constexpr uint32_t kRedOff = kScaleOff + kStages * kScales;
   static constexpr uint32_t kRedFloats = 8 * 8 * NT * D;  // [8 warps][8 NT heads][D]
@@ -134,7 +137,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // A (sequence, K/V head) pair's part of the run, the same walk for all warps.  A pair takes
 // `extra` + tiles units of the line: starting and joining it costs a CTA about as long as
-// `extra` tiles, so that a run of many short sequences gets fewer tiles.
+// `extra` tiles, so that a run of many short sequences gets fewer tiles.  A pair of at most
+// `extra` tiles is not cut between runs.
 struct Segment {
   int b, h, len, t0, nt, tiles;  // tiles [t0, t0 + nt) of the pair's `tiles`
   int first;                     // the line's unit at which the pair's tiles start
@@ -164,8 +168,13 @@ struct Walk {
       const int in = at - b_first;
       s.h = in / units;
       const int from = in - s.h * units, to = min(units, from + (end - at));
-      s.t0 = max(from - kExtra, 0);
-      s.nt = max(to - kExtra, 0) - s.t0;
+      if (tiles <= kExtra) {  // not cut: all of it where it starts (joining parts costs more)
+        s.t0 = 0;
+        s.nt = from == 0 ? tiles : 0;
+      } else {
+        s.t0 = max(from - kExtra, 0);
+        s.nt = max(to - kExtra, 0) - s.t0;
+      }
       s.first = at - from + kExtra;
       at += to - from;
       if (s.nt > 0) return true;
