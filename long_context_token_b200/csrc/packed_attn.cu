@@ -24,10 +24,11 @@
 // cycles of its special-function unit and about 740 with what cannot hide behind it, so two
 // tiles take 1480 cycles a step, in which the tensor pipe works 1090.  On a B200, one prompt
 // of 16384 tokens (16 heads, 2 K/V heads, d 128, bfloat16): 840 us, 1309 TFLOP/s, 0.79 of the
-// measured burst rate of a library product; 975 us when the call repeats until the power cap
-// lowers the clock (0.80 of the measured sustained rate).  What was measured on the way to
-// this shape, on that prompt: 128-key steps with one S buffer per tile 1040 us; the MMAs of
-// both tiles from one warp 942; without taking turns 878.
+// measured burst rate of a library product (up to 890 us on a warm GPU); 975 us when the call
+// repeats until the power cap lowers the clock (0.80 of the measured sustained rate).  What
+// was measured on the way to this shape, on that prompt: 128-key steps with one S buffer per
+// tile 1040 us; the MMAs of both tiles from one warp 942; without taking turns 878; two
+// threads per row 904.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product, as the MMA needs;
 // the row sums, references and O stay in float32.

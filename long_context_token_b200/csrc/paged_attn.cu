@@ -34,7 +34,7 @@
 // 10 us of latencies around them: the run and the first pages (3 us), the join within the CTA,
 // the arrival and the join of the parts (4 us).  On a B200, 8 x 131072 bfloat16 keys of one
 // K/V head under 16 query heads: 90 us, 5.94 TB/s, 0.91 of the measured copy rate; 64
-// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 97 us, 5.2 TB/s, 0.79.  Groups of 64
+// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 95 us, 5.3 TB/s, 0.81.  Groups of 64
 // and more heads are bound by the products and conversions, which every 16 heads repeat: one
 // sequence of 1048576 FP8 keys under 64 heads takes 190 us, 4.5 times its bytes' time.
 #include "paged.cuh"
