@@ -408,7 +408,9 @@ HS2_API size_t hs2_packed_workspace_bytes(void);
  *            or NULL.  A query that sees nothing gives out 0 and lse -inf.  Rows from
  *            cu_q[batch] on are left as they were.
  *   sm_scale finite and > 0.
- * Non-finite rows of K or V reach only queries of their own sequence, padding rows none.
+ * Logits that are NaN or +inf make the results of the queries that see their keys NaN; a
+ * query whose visible logits are all -inf gives 0 and -inf.  A non-finite V row may reach
+ * every query of its own sequence, and no other; padding rows reach none.
  * cu entries that descend or pass n_q / n_k set HS2_ERR_BAD_LENGTH and are clamped.  n_q 0
  * does nothing; n_q * h_q, n_k * n_kv_heads < 2^31; batch <= 65535. */
 HS2_API hs2_status hs2_packed_attn(const hs2_packed* p, float sm_scale, void* out, float* lse,

@@ -97,16 +97,18 @@ __host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 1
 
 // 2^x of two numbers at most about 2^7 on the multiply-add pipes: x = n + f with n the nearest
 // integer, 2^f by the polynomial of degree 4 with the least relative error on [-1/2, 1/2]
-// (2.6e-6, from the Remez exchange), n added to its exponent.  Of each kPairsOf pairs of
+// (2.6e-6, from the Remez exchange), times 2^n.  Of each kPairsOf pairs of
 // weights kPairsByFma are formed this way, to relieve the special-function units: one in
 // eight (none 862 us on the prompt above, one 841, two 855, three 865, four 887: the
 // multiply-add pipes and the issue slots are not free either).
 constexpr int kPairsOf = 8, kPairsByFma = 1;
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
-  x.x = fmaxf(x.x, -126.f);  // (smaller ones give 2^-126: nothing next to the row's sum)
-  x.y = fmaxf(x.y, -126.f);
-  const float2 magic = make_float2(12582912.f, 12582912.f);  // 1.5 x 2^23: its sums are integers
-  const float2 minus = make_float2(-12582912.f, -12582912.f), one = make_float2(-1.f, -1.f);
+  // (Below -126.5 the factor 2^n is 0, so a masked key weighs nothing; a NaN stays one.)
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
+  // 1.5 x 2^23 + 127: the low bits of its sum with x are n + 127, the exponent of 2^n.
+  const float2 magic = make_float2(12583039.f, 12583039.f);
+  const float2 minus = make_float2(-12583039.f, -12583039.f), one = make_float2(-1.f, -1.f);
   const float2 t = add2(x, magic);
   const float2 f = fma2(add2(t, minus), one, x);
   auto both = [](float v) { return make_float2(v, v); };
@@ -114,8 +116,8 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
   y = fma2(y, f, both(0x1.ec06dap-3f));
   y = fma2(y, f, both(0x1.62e0dcp-1f));
   y = fma2(y, f, both(0x1.ffffe8p-1f));
-  return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23)));
+  return mul2(y, make_float2(__uint_as_float(__float_as_uint(t.x) << 23),
+                             __uint_as_float(__float_as_uint(t.y) << 23)));
 }
 
 }  // namespace
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       }
       if (!ok) break;
       const bool any = seen > 0;
-      const float inv = any ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // (0: every logit is -inf)
       const size_t row = (size_t)(it.q_row + t * tpt + tok) * p.h_q + it.head * p.group + hh;
       uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * (D * 2));
       if (steps > 0) {

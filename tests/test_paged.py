@@ -363,6 +363,12 @@ def test_step_large_and_peaked_logits(kv):
     run_step(pool, 16, "bf16", scale=1.0)
 
 
+def inf_logits(q, k):
+    """Makes q . k -inf for the rows k (every other element of theirs is finite)."""
+    q[..., 0] = 1.0
+    k[..., 0] = -math.inf
+
+
 @pytest.mark.gpu
 def test_step_scales_of_all_sizes():
     """FP8 rows of V whose scales span 2^-40 .. 2^40 and 0: each weight is held relative to
@@ -536,6 +542,60 @@ def test_prompt_garbage_stays_in_its_sequence(heads):
     out, _ = hs2.packed_attn(q, k, v, cu, workspace=ws)
     for rows in (slice(0, 100), slice(161, 291)):
         assert same(out[rows], clean[rows].cpu())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("h_q,h_kv", [(4, 2), (40, 40)])  # one and two tiles per work item
+def test_prompt_logits_of_minus_infinity(dtype, h_q, h_kv):
+    """Keys with a logit of -inf have no weight; a row of only such keys gives zeros and -inf."""
+    n, dead, d = 300, 140, 64
+    g = torch.Generator().manual_seed(45)
+    q, k, v = (torch.randn(n, h, d, generator=g).to(TYPES[dtype]) for h in (h_q, h_kv, h_kv))
+    inf_logits(q, k[:dead])
+    ws = hs2.packed_workspace(DEV)
+    out, lse = hs2.packed_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu_of([n]).to(DEV), workspace=ws)
+    assert hs2.check_device_status(ws) == 0
+    assert bool((out[:dead] == 0).all()) and bool((lse[:dead] == -math.inf).all())
+    check_prompts(q[dead:], k[dead:], v[dead:], [n - dead], [n - dead], out[dead:], lse[dead:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("h_q,h_kv", [(4, 2), (40, 40)])
+@pytest.mark.parametrize("at", [0, 3, 14, 79, 142, 270])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_prompt_keeps_nan(dtype, d, h_q, h_kv, at, value):
+    """A NaN or +inf logit makes the results NaN of the queries that see its key, whichever key
+    it is, and of no query before it."""
+    n = 300
+    g = torch.Generator().manual_seed(46)
+    q, k, v = (torch.randn(n, h, d, generator=g).to(TYPES[dtype]) for h in (h_q, h_kv, h_kv))
+    q[..., 0] = 1.0
+    cu, ws = cu_of([n]).to(DEV), hs2.packed_workspace(DEV)
+    clean, clean_lse = hs2.packed_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu, workspace=ws)
+    k[at, :, 0] = value
+    out, lse = hs2.packed_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu, workspace=ws)
+    assert hs2.check_device_status(ws) == 0
+    assert same(out[:at], clean[:at].cpu()) and same(lse[:at], clean_lse[:at].cpu())
+    assert bool(torch.isnan(out[at:]).all()) and bool(torch.isnan(lse[at:]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("h_q,h_kv", [(4, 2), (40, 40)])
+def test_prompt_large_values_behind_the_mask(dtype, h_q, h_kv):
+    """The largest finite V behind a query's mask adds nothing to it."""
+    n, d = 300, 128
+    g = torch.Generator().manual_seed(47)
+    q, k, v = (torch.randn(n, h, d, generator=g).to(TYPES[dtype]).to(DEV) for h in (h_q, h_kv, h_kv))
+    cu, ws = cu_of([n]).to(DEV), hs2.packed_workspace(DEV)
+    clean, clean_lse = hs2.packed_attn(q, k, v, cu, workspace=ws)
+    for at in (1, 70, 200):
+        big = v.clone()
+        big[at:] = torch.finfo(v.dtype).max
+        out, lse = hs2.packed_attn(q, k, big, cu, workspace=ws)
+        assert same(out[:at], clean[:at].cpu()) and same(lse, clean_lse.cpu())
 
 
 @pytest.mark.gpu
