@@ -367,7 +367,8 @@ HS2_API hs2_status hs2_paged_kv_read(const hs2_paged_kv* kv, const int32_t* cu,
  *   out      device, type `dtype`, [batch][h_q][head_dim]: softmax(sm_scale q.k) @ V over
  *            positions [0, lens[b]).
  *   lse      device float32 [batch][h_q], natural log, or NULL.
- * An empty sequence gives out 0 and lse -inf.  A bad page's keys count as page 0's (the
+ * An empty sequence, and one whose logits are all -inf, gives out 0 and lse -inf; a logit of
+ * NaN or +inf makes its sequence's out and lse of that head NaN.  A bad page's keys count as page 0's (the
  * sequence's result is then meaningless; no access leaves the cache).  The work is split
  * over the keys of all sequences and joined in a fixed order: repeated runs on the same
  * inputs are bitwise identical. */

@@ -214,8 +214,8 @@ __device__ __noinline__ void join_parts(float* partials, int part_floats, int fi
       fetch(0);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < k) ml = __ldcg(reinterpret_cast<const float2*>(part(from + lane) + group * D + 2 * hr));
-      const float top = fmaxf(mm, warp_max(ml.x));  // finite: every part holds a key
-      const float keep = ex2_ftz(mm - top), w = ex2_ftz(ml.x - top);
+      const float top = fmaxf(mm, warp_max(ml.x)), ref = finite_ref(top);  // (-inf: all logits are)
+      const float keep = ex2_ftz(mm - ref), w = ex2_ftz(ml.x - ref);
       ll = fmaf(ll, keep, warp_sum(w * ml.y));
       mm = top;
 #pragma unroll
@@ -234,11 +234,11 @@ __device__ __noinline__ void join_parts(float* partials, int part_floats, int fi
       }
     }
     if (out_rows) {
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      const float inv = ll != 0.f ? 1.f / ll : 0.f;  // (a NaN stays one)
       uint32_t* out = reinterpret_cast<uint32_t*>(out_rows + (size_t)hr * (D * 2)) + lane * (E / 2);
 #pragma unroll
       for (int x = 0; x < E / 2; ++x) out[x] = pack2<Q>(v[2 * x] * inv, v[2 * x + 1] * inv);
-      if (lse && lane == 0) lse[hr] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+      if (lse && lane == 0) lse[hr] = ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     } else {
       // (this warp has read all of the head's parts)
       float* to = part(0);
@@ -766,10 +766,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       };
       float* part = part_of(blockIdx.x, s.t0 == 0);
       auto emit = [&](int hr, int d, float4 v, float m, float l) {  // a finished row's four elements
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         uint2 w = make_uint2(pack2<Q>(v.x * inv, v.y * inv), pack2<Q>(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + (head0 + hr) * (D * 2) + d * 2) = w;
-        if (d == 0 && p.lse) p.lse[head0 + hr] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (d == 0 && p.lse) p.lse[head0 + hr] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       };
       auto join = [&](auto warps_of_a_head) {
         constexpr int N = decltype(warps_of_a_head)::value;

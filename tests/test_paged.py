@@ -370,6 +370,51 @@ def inf_logits(q, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kv,h_q,h_kv", [("bf16", 2, 1), ("f16", 16, 1), ("f16", 64, 1), ("bf16", 8, 8)])
+def test_step_logits_of_minus_infinity(kv, h_q, h_kv):
+    """Keys with a logit of -inf have no weight, in whatever parts a sequence is cut; a row of
+    only such keys gives zeros and -inf, as one without keys."""
+    lens, dead = [30000, 40, 30000, 200, 0], [20000, 40, 30000, 150, 0]
+    pool = Pool(lens, h_kv, 64, 16, kv, seed=41)
+    q = torch.randn(len(lens), h_q, 64, generator=torch.Generator().manual_seed(42)).to(TYPES[kv])
+    for b, n in enumerate(dead):
+        pg, r = pool.at(b, 0, n)
+        rows = pool.k[pg, :, r]
+        inf_logits(q, rows)
+        pool.k[pg, :, r] = rows
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache, h_q)
+    out, lse = (x.cpu() for x in hs2.paged_attn(q.to(DEV), cache, ws))
+    assert hs2.check_device_status(ws) == 0
+    g, scale = h_q // h_kv, float(torch.tensor(0.125))
+    for b, n in enumerate(lens):
+        k, v = pool.rows(b, dead[b], n)  # the others are as if they were not there
+        for h in range(h_kv):
+            hs = slice(h * g, (h + 1) * g)
+            ref = attend(q[b, hs].double(), k[:, h], v[:, h], scale, torch.full((g,), n - dead[b]))
+            check(out[b, hs], lse[b, hs], ref, q.dtype, q.dtype, n, f"sequence {b}, head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,value", [("bf16", math.nan), ("f16", math.nan), ("fp8", math.nan),
+                                      ("bf16", math.inf), ("f16", math.inf)])
+def test_step_keeps_nan(kv, value):
+    """A NaN or +inf logit makes its sequence's results NaN, the lse included, and no other's."""
+    pool = Pool([30000, 50, 60, 20000], 1, 128, 32, kv, seed=43)
+    for b, at in ((0, 17001), (1, 31)):
+        pg, r = pool.at(b, at, at + 1)
+        pool.k[pg, 0, r, 5] = 0x7F if kv == "fp8" else value
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache, 16)
+    qt = torch.float16 if kv == "f16" else torch.bfloat16
+    q = torch.randn(4, 16, 128, generator=torch.Generator().manual_seed(44)).to(qt)
+    q[..., 5] = 1.0
+    out, lse = hs2.paged_attn(q.to(DEV), cache, ws)
+    for b, bad in enumerate((True, True, False, False)):
+        assert bool((torch.isnan(out[b]) == bad).all()) and bool((torch.isnan(lse[b]) == bad).all())
+
+
+@pytest.mark.gpu
 def test_step_scales_of_all_sizes():
     """FP8 rows of V whose scales span 2^-40 .. 2^40 and 0: each weight is held relative to
     the largest weight times scale."""
