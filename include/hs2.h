@@ -335,7 +335,8 @@ HS2_API size_t hs2_paged_workspace_bytes(const hs2_paged_kv* kv, int h_q);
  *             ignored.  NULL: n_tokens / batch tokens for every sequence (n_tokens must be
  *             a multiple of batch).
  * FP8 rows (one token, one head) get the scale and codes of hs2_kv_append: s = amax / 448
- * (1 for a zero row), code = row / s, both divisions IEEE float32, saturating.
+ * (1 for a zero row; NaN elements do not count), code = row / s, both divisions IEEE
+ * float32, saturating, a NaN either of the NaN codes.
  * A sequence with lens[b] < n_b or a bad length is left unwritten (HS2_ERR_BAD_LENGTH), a
  * row with a bad page too (HS2_ERR_INDEX_OUT_OF_RANGE).  Two tokens for one slot: either's
  * row, or parts of both.  n_tokens 0 does nothing; n_tokens * n_kv_heads < 2^31. */

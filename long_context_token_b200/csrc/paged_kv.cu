@@ -76,7 +76,8 @@ __device__ __forceinline__ uint32_t e4m3_pair(float2 y) {
 // -x / s, correctly rounded, from nr = -1 / s rounded: the product is within 1.5 units in the
 // last place, so within one after the first correction and rounded correctly after the
 // second.  (The negated quotient keeps the sign of zeros through the corrections.)  Every
-// remainder that matters is exact while s is at least 2^-60; smaller rows are divided out.
+// remainder that matters is exact while s is finite and at least 2^-60; other rows are
+// divided out.
 __device__ __forceinline__ float2 minus_quotient(float2 x, float2 s, float2 nr) {
   float2 y = mul2(x, nr);
   y = fma2(fma2(y, s, x), nr, y);
@@ -167,12 +168,12 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) paged_move_kerne
     const float nr = -__frcp_rn(s);
     const float2 s2 = make_float2(s, s), nr2 = make_float2(nr, nr);
     uint32_t code[4];
-    if (s >= 0x1p-60f) {
+    if (s >= 0x1p-60f && s < INFINITY) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         code[e] = (e4m3_pair(minus_quotient(unpack2<T>(u[2 * e]), s2, nr2)) |
                    (e4m3_pair(minus_quotient(unpack2<T>(u[2 * e + 1]), s2, nr2)) << 16)) ^ 0x80808080u;
-    } else {  // tiny rows, and NaN
+    } else {  // tiny rows, and rows with an infinity
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 x = unpack2<T>(u[2 * e]), z = unpack2<T>(u[2 * e + 1]);

@@ -241,6 +241,31 @@ def test_quotients_at_the_middle_between_codes(src):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("src", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_of_infinities_and_nan(src, d):
+    """The scale of a row ignores its NaN; codes are the IEEE quotients: x / inf is 0."""
+    x = torch.randn(6, 1, d, generator=torch.Generator().manual_seed(48)).to(TYPES[src])
+    x[1, 0, 5], x[2, 0, 60] = math.inf, -math.inf
+    x[3, 0, 7] = math.nan
+    x[4, 0, 0], x[4, 0, 50] = math.inf, math.nan
+    x[5] = math.nan
+    f = x[:, 0].float()
+    amax = f.abs().nan_to_num(0.0, posinf=math.inf).amax(-1)
+    s = torch.where(amax > 0, amax / torch.full_like(amax, 448.0), torch.ones_like(amax))
+    y = f / s[:, None]
+    codes = y.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    cache = cache_of(Pool([6], 1, d, 8, "fp8", empty=True))
+    hs2.paged_kv_write(x.to(DEV), x.to(DEV), cache, hs2.paged_workspace(cache))
+    pg = int(cache.pages[0, 0])
+    for got, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        assert same(scale[pg, 0, :6], s)
+        got = got[pg, 0, :6].cpu()
+        nan = torch.isnan(y)
+        assert bool(((got & 0x7F) == 0x7F)[nan].all()) and torch.equal(got[~nan], codes[~nan])
+
+
+@pytest.mark.gpu
 def test_uniform_write_is_the_packed_one():
     lens, n = [40, 9, 1024], 3
     a, b = (Pool(lens, 2, 128, 32, "fp8", seed=3, empty=True) for _ in range(2))
