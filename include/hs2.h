@@ -339,7 +339,7 @@ HS2_API size_t hs2_paged_workspace_bytes(const hs2_paged_kv* kv, int h_q);
  * float32, saturating, a NaN either of the NaN codes.
  * A sequence with lens[b] < n_b or a bad length is left unwritten (HS2_ERR_BAD_LENGTH), a
  * row with a bad page too (HS2_ERR_INDEX_OUT_OF_RANGE).  Two tokens for one slot: either's
- * row, or parts of both.  n_tokens 0 does nothing; n_tokens * n_kv_heads < 2^31. */
+ * row, or parts of both.  n_tokens 0 does nothing; n_tokens < (2^31 - 4096) / n_kv_heads. */
 HS2_API hs2_status hs2_paged_kv_write(const void* k_new, const void* v_new, int dtype,
                                       int64_t token_stride, int64_t head_stride, int n_tokens,
                                       const int32_t* cu_new, const hs2_paged_kv* kv,
@@ -352,7 +352,7 @@ HS2_API hs2_status hs2_paged_kv_write(const void* k_new, const void* v_new, int 
  *   k_out, v_out  device, row of token t and head h at t * token_stride + h * head_stride.
  * Rows from cu[batch] on, rows of positions outside [0, lens[b]) (HS2_ERR_BAD_LENGTH) and
  * rows of bad pages (HS2_ERR_INDEX_OUT_OF_RANGE) are left as they were.  n_tokens 0 does
- * nothing; n_tokens * n_kv_heads < 2^31. */
+ * nothing; n_tokens < (2^31 - 4096) / n_kv_heads. */
 HS2_API hs2_status hs2_paged_kv_read(const hs2_paged_kv* kv, const int32_t* cu,
                                      const int32_t* start, int n_tokens, void* k_out,
                                      void* v_out, int dtype, int64_t token_stride,
@@ -414,7 +414,7 @@ HS2_API size_t hs2_packed_workspace_bytes(void);
  * query whose visible logits are all -inf gives 0 and -inf.  A non-finite V row may reach
  * every query of its own sequence, and no other; padding rows reach none.
  * cu entries that descend or pass n_q / n_k set HS2_ERR_BAD_LENGTH and are clamped.  n_q 0
- * does nothing; n_q * h_q, n_k * n_kv_heads < 2^31; batch <= 65535. */
+ * does nothing; n_q < (2^31 - 4096) / h_q, n_k < (2^31 - 4096) / n_kv_heads; batch <= 65535. */
 HS2_API hs2_status hs2_packed_attn(const hs2_packed* p, float sm_scale, void* out, float* lse,
                                    void* workspace, size_t ws_bytes, hs2_stream_t stream);
 

@@ -6,6 +6,9 @@
 
 namespace hs2 {
 
+// Tokens times heads stay below this, so that counts rounded up to whole blocks fit an int.
+constexpr int kMaxRows = (1 << 30) + ((1 << 30) - 4096);
+
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 static bool is_16bit(int dtype) { return dtype == HS2_KV_BF16 || dtype == HS2_KV_F16; }
 
@@ -95,7 +98,7 @@ static hs2_status check_move(const hs2_paged_kv* kv, const void* k_rows, const v
   if (n_tokens && (!k_rows || !v_rows || !aligned16(k_rows) || !aligned16(v_rows)))
     return HS2_ERR_INVALID_ARGUMENT;
   if (!cu && n_tokens % kv->batch) return HS2_ERR_INVALID_ARGUMENT;
-  if ((long long)n_tokens * kv->n_kv_heads >= (1ll << 31)) return HS2_ERR_UNSUPPORTED;
+  if (n_tokens >= kMaxRows / kv->n_kv_heads) return HS2_ERR_UNSUPPORTED;
   if (ws_bytes < paged_bytes(kv, 0)) return HS2_ERR_WORKSPACE_TOO_SMALL;
   return HS2_OK;
 }
@@ -190,7 +193,7 @@ hs2_status hs2_packed_attn(const hs2_packed* a, float sm_scale, void* out, float
   if (a->batch < 1 || a->n_q < 0 || a->n_k < 0 || a->n_kv_heads < 1)
     return HS2_ERR_INVALID_ARGUMENT;
   if (a->n_kv_heads > 1024 || !check_heads(a->h_q, a->n_kv_heads) || a->batch > 65535 ||
-      (long long)a->n_q * a->h_q >= (1ll << 31) || (long long)a->n_k * a->n_kv_heads >= (1ll << 31))
+      a->n_q >= kMaxRows / a->h_q || a->n_k >= kMaxRows / a->n_kv_heads)
     return HS2_ERR_UNSUPPORTED;
   if (!check_scale(sm_scale) || !good_stride(a->q_token_stride, 2) ||
       !good_stride(a->q_head_stride, 2) || !good_stride(a->kv_token_stride, 2) ||

@@ -84,6 +84,20 @@ def test_write_and_read_refuse_bad_arguments(L, args, code):
                                a["ws"], a["ws_bytes"], None) == code
 
 
+@pytest.mark.parametrize("heads", [1, 2, 8])
+def test_row_counts_that_do_not_round_up_are_refused(L, heads):
+    """Counts are rounded up to whole blocks of up to a thousand rows in 32 bits."""
+    n = ((1 << 31) - 1000) // heads
+    kv = ctypes.byref(_kv(n_kv_heads=heads))
+    assert L.hs2_paged_kv_write(P, P, 0, 0, 128, n, P, kv, P, 1 << 20, None) == 2
+    assert L.hs2_paged_kv_read(kv, P, None, n, P, P, 0, 1024, 128, P, 1 << 20, None) == 2
+    f = dict(q=P, k=P, v=P, cu_q=P, cu_k=P, q_token_stride=1024, q_head_stride=128, kv_token_stride=8,
+             kv_head_stride=8, n_q=10, n_k=10, batch=2, h_q=heads, n_kv_heads=heads, head_dim=128, dtype=0)
+    for k in ("n_q", "n_k"):
+        a = hs2.Packed(**dict(f, **{k: n}))
+        assert L.hs2_packed_attn(ctypes.byref(a), 0.1, P, P, P, 1 << 20, None) == 2
+
+
 def test_nothing_to_move_is_no_error(L):
     kv = ctypes.byref(_kv())
     assert L.hs2_paged_kv_write(None, None, 0, 1024, 128, 0, P, kv, P, 4096, None) == 0
