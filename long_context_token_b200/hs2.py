@@ -617,7 +617,8 @@ def paged_kv_read(cache: PagedCache, cu: torch.Tensor, workspace: torch.Tensor,
         raise ValueError("k_out and v_out go together")
     if k_out is None:
         if n_tokens is None:
-            n_tokens = int(cu[-1])
+            with torch.cuda.stream(stream):  # (cu may have been written on it; None: the current one)
+                n_tokens = int(cu[-1])
         if dtype is None:
             dtype = torch.bfloat16 if cache.dtype == HS2_KV_FP8_E4M3 else cache.k.dtype
         k_out, v_out = (_new(stream, torch.zeros, n_tokens, cache.h_kv, cache.head_dim,
