@@ -510,13 +510,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       for (int n = 0; n < NT; ++n) {
         float g = 1.f;  // 1 / the power of two that this thread's head is multiplied by
         if constexpr (kScaleQ) {
-          float top = 0.f;
+          float top = 0.f;  // over the finite elements: an infinity stays one under any factor but 0
+          auto size = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const float2 x = unpack2<Q>(qb[k][n][u]);
-              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+              top = fmaxf(top, fmaxf(size(x.x), size(x.y)));
             }
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
