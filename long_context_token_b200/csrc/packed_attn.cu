@@ -30,8 +30,9 @@
 // tile 1040 us; the MMAs of both tiles from one warp 942; without taking turns 878; two
 // threads per row 904.
 //
-// Weights are rounded to the inputs' 16-bit type for the second product, as the MMA needs;
-// the row sums, references and O stay in float32.
+// Weights are rounded to the inputs' 16-bit type for the second product, as the MMA needs
+// (float16 ones scaled so that the largest lies in [2^7, 2^15]); the row sums, references and O
+// stay in float32.
 #include <string.h>
 
 #include "paged.cuh"
@@ -95,7 +96,7 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t tile) {
 }
 __host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 16 * 128 >> 4); }
 
-// 2^x of two numbers at most about 2^7 on the multiply-add pipes: x = n + f with n the nearest
+// 2^x of two numbers of up to about 100 on the multiply-add pipes: x = n + f with n the nearest
 // integer, 2^f by the polynomial of degree 4 with the least relative error on [-1/2, 1/2]
 // (2.6e-6, from the Remez exchange), times 2^n.  Of each kPairsOf pairs of
 // weights kPairsByFma are formed this way, to relieve the special-function units: one in
@@ -224,6 +225,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   using L = PackedSmem<D>;
   constexpr int NS = L::kStages;
   constexpr bool kBf16 = !std::is_same<T, __half>::value;
+  // Float16 weights are 2^7 times 2^(x - m): at most 2^15, as m lags by at most 8.  Without the
+  // factor those below 2^-25 of the reference vanished from the output but not from the sum.
+  constexpr float kLift = kBf16 ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* qs = smem + L::kQOff;
@@ -583,7 +587,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           }
         }
         take_turn();
-        const float ref = -finite_ref(m);
+        const float ref = kLift - finite_ref(m);
         const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
         for (int e = 0; e < D / 8; ++e) out[e] = make_uint4(0, 0, 0, 0);
       }
-      if (live && p.lse) p.lse[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (live && p.lse) p.lse[row] = any ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
     }
     __threadfence();  // the results are visible before the next kernel may start
   }

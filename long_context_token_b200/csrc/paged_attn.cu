@@ -21,9 +21,11 @@
 //                  shared memory when a (sequence, head) pair ends.
 //
 // The softmax reference moves only when a logit passes it by more than 8 (log2 units), so a
-// tile has no shuffles.  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
-// with m following max(x + log2 s_v), so w <= 2^8 is rounded to float16 relative to the
-// largest weight however the scales vary; E4M3 codes are exact in float16.  A bfloat16
+// tile has no shuffles.  A weight is rounded once, to the type of the second product: bfloat16,
+// or float16 scaled so that the largest lies in [2^7, 2^15], half a step each down to 2^-21 of
+// it and 2^-32 of it below.  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
+// with m following max(x + log2 s_v), so w is rounded to float16 relative to the largest weight
+// however the scales vary; E4M3 codes are exact in float16.  A bfloat16
 // query against codes is brought to float16 by a power of two per head, exactly down to
 // 2^-29 of its largest element.
 //
@@ -260,6 +262,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   constexpr int RB = L::kRowBytes;
   constexpr bool kBf16 = !kFp8 && !std::is_same<Q, __half>::value;  // the MMAs' type
   constexpr bool kScaleQ = kFp8 && !std::is_same<Q, __half>::value;
+  // Float16 weights are 2^7 times 2^(x - m): at most 2^15, as m lags by at most 8.  Without the
+  // factor those below 2^-25 of the reference vanished from the output but not from the sum.
+  constexpr float kLift = kBf16 ? 0.f : 7.f;
   constexpr int KS = D / 16;  // MMA steps along D
   constexpr int HT = 8 * NT;  // heads of a warp
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float n0 = -finite_ref(m[n][0]), n1 = -finite_ref(m[n][1]);
+          const float n0 = kLift - finite_ref(m[n][0]), n1 = kLift - finite_ref(m[n][1]);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -742,7 +747,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
           const int row = warp * HT + n * 8 + 2 * c4 + e;
-          if (r8 == 0) red_ml[row] = make_float2(m[n][e], x);
+          if (r8 == 0) red_ml[row] = make_float2(m[n][e] - kLift, x);
           // (elements xored with the head, to spread the heads over the banks)
           float* to = red + row * D;
           const int swz = c4 << 3;

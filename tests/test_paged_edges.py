@@ -6,8 +6,25 @@ import torch
 
 from long_context_token_b200 import hs2
 
-from _paged_ref import Pool, attend, check
+from _paged_ref import Pool, TYPES, attend, check
 from test_paged import DEV, cache_of, cu_of, same
+
+
+def half(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def bound(o, w_abs_v, mag, n, out_type, weight_type, lost=0.0):
+    """How far a result may be from its definition: a float32 logit is off by at most
+    e = 160 * 2^-24 of `mag` (the largest sum |q_i k_i| * scale) + 1, which moves a weight and the
+    sum of the weights by at most 2.1 e each; a weight is rounded once; the products of 16 keys
+    at a time enter the sum one after another, each addition off by at most 2^-23 of what it has
+    (the weights' own sum the same); the quotient's two roundings and the result's own.  `lost`:
+    what roundings of weights below the normal numbers of their type may add up to."""
+    e = 160 * 2.0 ** -24 * (mag + 1)
+    rel = half(weight_type) + 4.2 * e + 2 * (n / 16 + 8) * 2.0 ** -23
+    own = half(out_type) * (o.abs() + rel * w_abs_v + lost) + torch.finfo(out_type).smallest_normal * half(out_type)
+    return rel * w_abs_v + lost + own
 
 
 @pytest.mark.gpu
@@ -57,3 +74,56 @@ def test_step_of_a_query_with_an_infinity_over_codes(d, h_q):
             if (b, h) not in ((0, 0), (1, 1)):
                 ref = attend(q[b, h:h + 1].double(), k[:, 0], v[:, 0], scale, torch.tensor([n]))
                 check(out[b, h:h + 1], lse[b, h:h + 1], ref, torch.bfloat16, torch.float16, n)
+
+
+def sinks(n, d, h_kv, h_q, gap, every, dtype, seed):
+    """Rows of n keys of which one, or one of `every`, has a logit `gap` above all others'
+    (which are 0) and a V of zeros: the result is what the others add up to.  sm_scale is 1."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(1, h_q, d, generator=g)
+    q[..., 0] = 1.0
+    k = torch.zeros(n, h_kv, d)
+    v = torch.rand(n, h_kv, d, generator=g) * 1000 + 500
+    at = torch.arange(0, n, every or n)
+    k[at, :, 0] = gap
+    v[at] = 0
+    return q.to(dtype), k.to(dtype), v.to(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,h_q,h_kv,gap,every", [(128, 4, 2, 18.5, None), (128, 4, 1, 18.5, 7),
+                                                  (64, 16, 16, 17.0, 5), (64, 34, 2, 12.0, None)])
+def test_small_weights_of_long_contexts_count(dtype, d, h_q, h_kv, gap, every):
+    """Weights down to 2^-27 of the largest.  A float16 weight below 2^-14 is off by at most
+    2^-25, and the largest lies in [2^7, 2^15]: 2^-32 of it.  The step over pages, and queries
+    after a prefix (one and two tiles per work item)."""
+    n, dt = 50001, TYPES[dtype]
+    q, k, v = sinks(n, d, h_kv, h_q, gap, every, dt, seed=53)
+    g = h_q // h_kv
+
+    def hold(out, lse, n):
+        for h in range(h_kv):
+            hs = slice(h * g, (h + 1) * g)
+            vv = v[:n, h].double()
+            o, z, a, mag = attend(q[0, hs].double(), k[:n, h].double(), vv, 1.0, torch.full((g,), n))
+            lost = 2.0 ** -32 * torch.exp(gap - z)[:, None] * vv.sum(0) if dtype == "f16" else 0.0
+            assert bool(((out[hs].cpu().double() - o).abs() <= bound(o, a, mag, n, dt, dt, lost)).all())
+            assert bool(((lse[hs].cpu().double() - z).abs() <= 1e-3).all())
+
+    cache = cache_of(Pool([n], h_kv, d, 64, dtype, seed=54, empty=True))
+    ws, pws = hs2.paged_workspace(cache, h_q), hs2.packed_workspace(DEV)
+    kd, vd = k.to(DEV), v.to(DEV)
+    hs2.paged_kv_write(kd, vd, cache, ws)
+    out, lse = hs2.paged_attn(q.to(DEV), cache, ws, 1.0)
+    hold(out[0], lse[0], n)
+    # (the last of three queries sees all keys)
+    out, lse = hs2.packed_attn(q.to(DEV).repeat(3, 1, 1), kd, vd, cu_of([3]).to(DEV), cu_of([n]).to(DEV), pws, 1.0)
+    hold(out[2], lse[2], n)
+    reps, short = 150, 3001  # the same keys for many sequences: more work items than SMs
+    cu = torch.arange(reps + 1, dtype=torch.int32, device=DEV)
+    out, lse = hs2.packed_attn(q.to(DEV).repeat(reps, 1, 1), kd[:short].repeat(reps, 1, 1),
+                               vd[:short].repeat(reps, 1, 1), cu, cu * short, pws, 1.0)
+    for b in (0, reps - 1):
+        hold(out[b], lse[b], short)
+    assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
