@@ -24,8 +24,8 @@
 // tile has no shuffles.  A weight is rounded once, to the type of the second product: bfloat16,
 // or float16 scaled so that the largest lies in [2^7, 2^15], half a step each down to 2^-21 of
 // it and 2^-32 of it below.  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
-// with m following max(x + log2 s_v), so w is rounded to float16 relative to the largest weight
-// however the scales vary; E4M3 codes are exact in float16.  A bfloat16
+// with m following max(x + log2 s_v) over the rows of V that are not all zeros, so w is rounded
+// to float16 relative to the largest weight however the scales vary; E4M3 codes are exact in float16.  A bfloat16
 // query against codes is brought to float16 by a power of two per head, exactly down to
 // 2^-29 of its largest element.
 //
@@ -60,6 +60,7 @@ constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
 constexpr int kJoinAtOnce = 512;  // rows (heads x partial results) that one CTA joins alone
 constexpr int kMinTiles = 8;  // a run is at least a tile for each warp
 constexpr float kMoveAt = 8.0f;
+constexpr float kNoScale = -64.f;  // log2 that stands for a V scale of 0 (and any below 2^-64)
 constexpr float kLn2 = 0.69314718055994531f;
 
 // NT: 8-head tiles per warp.
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if constexpr (kFp8) {
               kk = ks[key];
               vs[i][u] = ks[kTileKeys + key];
-              ref_by[i][u] = fmaxf(lg2(vs[i][u]), -64.f);
+              ref_by[i][u] = fmaxf(lg2(vs[i][u]), kNoScale);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -630,21 +631,48 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               }
         }
         float top[NT][2];
-        bool move = false;
+        auto any_moves = [&]() {
+          bool move = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x[4];
+            for (int e = 0; e < 2; ++e) {
+              float x[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              x[u] = sc[u >> 1][n][2 * (u & 1) + e];
-              if constexpr (kFp8) x[u] += ref_by[u >> 1][u & 1];
+              for (int u = 0; u < 4; ++u) {
+                x[u] = sc[u >> 1][n][2 * (u & 1) + e];
+                if constexpr (kFp8) x[u] += ref_by[u >> 1][u & 1];
+              }
+              top[n][e] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+              move = move || top[n][e] - m[n][e] > kMoveAt;
             }
-            top[n][e] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            move = move || top[n][e] - m[n][e] > kMoveAt;
+          return (bool)__any_sync(0xffffffffu, move);
+        };
+        bool moves = any_moves();
+        if (kFp8 && moves) {
+          // A row of zeros in V adds nothing whatever its scale (1, from hs2_paged_kv_write): it
+          // must not take the reference along, so it counts as one with scale 0.
+          uint32_t bits = 0;
+#pragma unroll
+          for (int c = 0; c < RB / 16; ++c) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(vt + at(lane, c)));
+            bits |= w[0] | w[1] | w[2] | w[3];
           }
-        if (__any_sync(0xffffffffu, move)) {
+          const uint32_t zero = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) == 0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (zero >> (16 * i + 8 * u + r8) & 1) {
+                vs[i][u] = 0.f;
+                ref_by[i][u] = kNoScale;
+              }
+          if (zero) moves = any_moves();
+        }
+        if (moves) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -127,3 +127,89 @@ def test_small_weights_of_long_contexts_count(dtype, d, h_q, h_kv, gap, every):
     for b in (0, reps - 1):
         hold(out[b], lse[b], short)
     assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
+
+
+def check_codes(pool, q, out, lse, scale, what=""):
+    """Results over an FP8 pool.  A weight times its V scale is off by half a step of float16,
+    or by 2^-32 of the largest such product over rows of V that are not all zeros."""
+    g = q.shape[1] // pool.h_kv
+    for b, n in enumerate(pool.lens):
+        k, v = pool.rows(b, 0, n)
+        pg, r = pool.at(b, 0, n)
+        for h in range(pool.h_kv):
+            hs = slice(h * g, (h + 1) * g)
+            qq = q[b, hs].double()
+            o, z, a, mag = attend(qq, k[:, h], v[:, h], scale, torch.full((g,), n))
+            w = torch.exp((qq @ k[:, h].T) * scale - z[:, None])  # [g, n]
+            vs = pool.v_scale[pg, h, r].double()
+            codes = pool.v[pg, h, r].view(torch.float8_e4m3fn).double().abs()
+            live = codes.amax(-1) > 0
+            top = (w * vs * live).amax(-1) if n else torch.zeros(g).double()
+            lost = 2.0 ** -32 * top[:, None] * codes.sum(0)
+            lim = bound(o, a, mag, n, q.dtype, torch.float16, lost)
+            off = (out[b, hs].cpu().double() - o).abs()
+            assert bool((off <= lim).all()), f"{what} sequence {b}, head {h}: {(off / lim).max().item()} of the bound"
+            # the weights' float32 sum, and the logits' own error
+            far = 4.2 * 160 * 2.0 ** -24 * (mag + 1) + (n / 16 + 8) * 2.0 ** -23 + 2.0 ** -20 * (1 + z.abs())
+            assert bool(((lse[b, hs].cpu().double() - z).abs() <= far).all()), what
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,h_q,h_kv", [(128, 8, 1), (64, 4, 2), (128, 32, 1)])
+@pytest.mark.parametrize("gap", [12.8, 13.5, 25.0, 40.0])
+def test_zero_rows_of_v_take_nothing_from_the_others(d, h_q, h_kv, gap):
+    """The library's own write gives a row of zeros the scale 1, a hundred times an ordinary
+    row's.  Such a row under a dominant logit (a sink) leaves the other keys their weights:
+    one in a cut sequence, some in whole ones, and a sequence that has no other rows."""
+    lens = [100000, 300, 33, 5000]
+    pool = Pool(lens, h_kv, d, 32, "fp8", seed=55, empty=True)
+    g = torch.Generator().manual_seed(56)
+    t = sum(lens)
+    k, v = (torch.randn(t, h_kv, d, generator=g) for _ in range(2))
+    k[..., 0] = 0
+    zero = [0, 100000 + 20, 100000 + 299] + list(range(100300, 100333)) + list(range(100333, 105333, 7))
+    k[zero] = 0
+    k[zero, :, 0] = gap / 2
+    v[zero] = 0
+    q = torch.randn(len(lens), h_q, d, generator=g) * 0.03
+    q[..., 0] = 2.0
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache, h_q)
+    hs2.paged_kv_write(k.to(DEV), v.to(DEV), cache, ws, cu_new=cu_of(lens).to(DEV))
+    pool.k, pool.v, pool.k_scale, pool.v_scale = (x.cpu() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale))
+    assert bool((pool.v_scale[pool.at(0, 0, 1)[0], :, pool.at(0, 0, 1)[1]] == 1).all())
+    out, lse = hs2.paged_attn(q.to(DEV), cache, ws, 1.0)
+    assert hs2.check_device_status(ws) == 0
+    check_codes(pool, q, out, lse, 1.0, f"gap {gap}")
+    assert bool((out[2] == 0).all())
+    # negative zeros are zeros
+    cache.v[(cache.v == 0)] = 0x80
+    out2, lse2 = hs2.paged_attn(q.to(DEV), cache, ws, 1.0)
+    assert same(lse2, lse.cpu()) and torch.equal(out2, out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,h_q,h_kv", [(128, 8, 1), (64, 34, 2)])
+def test_scales_of_v_mixed_within_a_sequence(d, h_q, h_kv):
+    """V scales over 2^-20 .. 2^20 within each sequence, under flat and under steep logits, and
+    a row of small codes with a large scale beside rows of large codes with small ones."""
+    for flat in (True, False):
+        pool = Pool([60000, 333, 32], h_kv, d, 16, "fp8", seed=57)
+        g = torch.Generator().manual_seed(58)
+        for b, n in enumerate(pool.lens):
+            pg, r = pool.at(b, 0, n)
+            pool.v_scale[pg, :, r] = 2.0 ** (40 * torch.rand(n, h_kv, generator=g) - 20)
+            if b == 0:  # most rows' scales are 2^-27 of some that are zero except in their first elements
+                pool.v_scale[pg, :, r] = 2.0 ** -27
+                pool.v[pg, :, r] = 0x7E  # 448
+                one, row = pg[5::32], r[5::32]
+                pool.v_scale[one, :, row] = 1.0
+                pool.v[one, :, row] = 0
+                pool.v[one, :, row, :3] = 0x38
+        q = torch.randn(3, h_q, d, generator=g).to(torch.bfloat16) * (0.0 if flat else 1.0)
+        cache = cache_of(pool)
+        ws = hs2.paged_workspace(cache, h_q)
+        out, lse = hs2.paged_attn(q.to(DEV), cache, ws)
+        assert hs2.check_device_status(ws) == 0
+        check_codes(pool, q, out, lse, float(torch.tensor(1 / math.sqrt(d), dtype=torch.float32)), f"flat {flat}")
