@@ -213,3 +213,60 @@ def test_scales_of_v_mixed_within_a_sequence(d, h_q, h_kv):
         out, lse = hs2.paged_attn(q.to(DEV), cache, ws)
         assert hs2.check_device_status(ws) == 0
         check_codes(pool, q, out, lse, float(torch.tensor(1 / math.sqrt(d), dtype=torch.float32)), f"flat {flat}")
+
+
+CUT = [  # (h_q, h_kv, d, lengths) whose sequences are cut into many parts, joined at once or in groups
+    (16, 1, 128, [131072] * 2), (3, 1, 64, [90001, 1, 100000]), (64, 1, 128, [120011, 3]),
+    (128, 1, 64, [70001]), (20, 1, 128, [150000]), (4, 4, 64, [9001, 77, 0, 12345]), (8, 2, 128, [40000, 1333]),
+]
+BLOCK = 97  # keys in a row with the same V
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("h_q,h_kv,d,lens", CUT)
+def test_every_part_of_a_cut_sequence_counts_once(kv, h_q, h_kv, d, lens):
+    """Each V row is 1 in one element, which moves with the key and the head.  Under equal
+    logits every sum is a whole number that float32 holds, so a result is the count of its
+    keys over their number, rounded; a lost, doubled or misplaced part of a sequence moves
+    many elements by a tenth.  Under random logits the results stay sums of positive terms,
+    held by their relative error alone."""
+    pool = Pool(lens, h_kv, d, 32, kv, seed=59)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        pg, r = pool.at(b, 0, n)
+        at = (torch.arange(n)[:, None] // BLOCK + 5 * torch.arange(h_kv) + b) % d  # [n, h_kv]
+        hot = torch.nn.functional.one_hot(at, d)
+        if kv == "fp8":
+            pool.v[pg, :, r] = (hot * 0x38).to(torch.uint8)
+            pool.v_scale[pg, :, r] = 1.0
+        else:
+            pool.v[pg, :, r] = hot.to(pool.v.dtype)
+    cache = cache_of(pool)
+    ws = hs2.paged_workspace(cache, h_q)
+    qt = torch.float16 if kv == "f16" else torch.bfloat16
+    wt = torch.float16 if kv == "fp8" else qt
+    scale = float(torch.tensor(1 / math.sqrt(d), dtype=torch.float32))
+    g = h_q // h_kv
+    for flat in (True, False):
+        q = torch.randn(len(lens), h_q, d, generator=torch.Generator().manual_seed(60)).to(qt) * (0.0 if flat else 1.0)
+        out, lse = (x.cpu().double() for x in hs2.paged_attn(q.to(DEV), cache, ws))
+        assert hs2.check_device_status(ws) == 0
+        for b, n in enumerate(lens):
+            if n == 0:
+                assert bool((out[b] == 0).all())
+                continue
+            k, v = pool.rows(b, 0, n)
+            for h in range(h_kv):
+                hs = slice(h * g, (h + 1) * g)
+                if flat:  # a reciprocal, a product and a rounding to 16 bits
+                    want = v[:, h].sum(0).expand(g, d) / n
+                    lim = (half(qt) + 2.0 ** -22) * want + 2.0 ** -25
+                    assert bool(((lse[b, hs] - math.log(n)).abs() < 1e-5).all())
+                else:
+                    want, z, _, mag = attend(q[b, hs].double(), k[:, h], v[:, h], scale, torch.full((g,), n))
+                    lim = bound(want, want, mag, n, qt, wt, n * 2.0 ** -32 if wt == torch.float16 else 0.0)
+                    assert bool((lim < 0.02 * want + 1e-4).all())  # a part is a hundredth of a sequence, at least
+                off = (out[b, hs] - want).abs()
+                assert bool((off <= lim).all()), f"sequence {b}, head {h}, flat {flat}"
