@@ -364,7 +364,7 @@ HS2_API hs2_status hs2_paged_kv_read(const hs2_paged_kv* kv, const int32_t* cu,
  *   q        device, type `dtype` (HS2_KV_BF16 or HS2_KV_F16; the cache's own type unless
  *            it is FP8), head h of sequence b at b * q_seq_stride + h * q_head_stride,
  *            16-byte aligned.
- *   sm_scale finite and > 0.
+ *   sm_scale > 0 and finite, its product with log2(e) too (below 2.35e38).
  *   out      device, type `dtype`, [batch][h_q][head_dim]: softmax(sm_scale q.k) @ V over
  *            positions [0, lens[b]).
  *   lse      device float32 [batch][h_q], natural log, or NULL.
@@ -409,7 +409,7 @@ HS2_API size_t hs2_packed_workspace_bytes(void);
  *   out      device, type dtype, [n_q][h_q][head_dim]; lse float32 [n_q][h_q], natural log,
  *            or NULL.  A query that sees nothing gives out 0 and lse -inf.  Rows from
  *            cu_q[batch] on are left as they were.
- *   sm_scale finite and > 0.
+ *   sm_scale > 0 and finite, its product with log2(e) too (below 2.35e38).
  * Logits that are NaN or +inf make the results of the queries that see their keys NaN; a
  * query whose visible logits are all -inf gives 0 and -inf.  A non-finite V row may reach
  * every query of its own sequence, and no other; padding rows reach none.

@@ -52,7 +52,8 @@ static bool check_heads(int h_q, int h_kv) {
   return h_q >= 1 && h_q % h_kv == 0 && h_q / h_kv <= 128;
 }
 
-static bool check_scale(float s) { return isfinite(s) && s > 0.f; }
+constexpr float kLog2e = 1.4426950408889634f;
+static bool check_scale(float s) { return isfinite(s * kLog2e) && s > 0.f; }
 
 static size_t paged_bytes(const hs2_paged_kv* kv, int h_q) {
   if (!h_q) return kPagedCounterOff;
@@ -174,7 +175,7 @@ hs2_status hs2_paged_attn(const void* q, int dtype, int h_q, int64_t q_seq_strid
   p.q_head = q_head_stride * 2;
   p.h_q = h_q;
   p.group = h_q / kv->n_kv_heads;
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.scale_log2 = sm_scale * kLog2e;
   p.out = out;
   p.lse = lse;
   p.counters = ws_ptr<uint32_t>(workspace, kPagedCounterOff);
@@ -224,7 +225,7 @@ hs2_status hs2_packed_attn(const hs2_packed* a, float sm_scale, void* out, float
   p.h_q = a->h_q;
   p.h_kv = a->n_kv_heads;
   p.group = a->h_q / a->n_kv_heads;
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.scale_log2 = sm_scale * kLog2e;
   p.out = out;
   p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);

@@ -1,4 +1,5 @@
 """Paged caches and packed prompts at the edges of what their definitions allow."""
+import ctypes
 import math
 
 import pytest
@@ -7,8 +8,20 @@ import torch
 from long_context_token_b200 import hs2
 
 from _paged_ref import Pool, TYPES, attend, check
-from test_paged import DEV, cache_of, cu_of, same
+from test_paged import DEV, L, P, _kv, cache_of, cu_of, same  # noqa: F401 (L is a fixture)
 
+
+# ---------------------------------------------------------------- the host's checks (CPU)
+@pytest.mark.parametrize("scale,code", [(3e38, 1), (2.36e38, 1), (-0.0, 1), (2.3e38, 3), (1e-45, 3)])
+def test_scales_that_float32_cannot_hold_in_log2_units_are_refused(L, scale, code):  # noqa: F811
+    """(A workspace that is too small, the last check, keeps the good ones from running.)"""
+    kv = _kv()
+    assert L.hs2_paged_attn(P, 0, 16, 2048, 128, ctypes.byref(kv), scale, P, P, P, 16, None) == code
+    p = hs2.Packed(P, P, P, P, P, 1024, 128, 256, 128, 10, 20, 2, 8, 2, 128, 0)
+    assert L.hs2_packed_attn(ctypes.byref(p), scale, P, P, P, 16, None) == code
+
+
+# ---------------------------------------------------------------- on the GPU
 
 def half(dtype):
     return torch.finfo(dtype).eps / 2
