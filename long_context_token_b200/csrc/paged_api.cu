@@ -12,8 +12,8 @@ constexpr int kMaxRows = (1 << 30) + ((1 << 30) - 4096);
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 static bool is_16bit(int dtype) { return dtype == HS2_KV_BF16 || dtype == HS2_KV_F16; }
 
-// Strides of rows of `elt`-byte elements: non-negative multiples of 16 bytes, small enough
-// that no offset formed from them passes 2^62 bytes.
+// Strides of rows of `elt`-byte elements: non-negative multiples of 16 bytes, below the 2^40
+// bytes that end a tensor map's strides.
 static bool good_stride(int64_t elements, int elt) {
   return elements >= 0 && elements < (int64_t(1) << 38) && elements * elt % 16 == 0;
 }
