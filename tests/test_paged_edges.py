@@ -283,3 +283,58 @@ def test_every_part_of_a_cut_sequence_counts_once(kv, h_q, h_kv, d, lens):
                     assert bool((lim < 0.02 * want + 1e-4).all())  # a part is a hundredth of a sequence, at least
                 off = (out[b, hs] - want).abs()
                 assert bool((off <= lim).all()), f"sequence {b}, head {h}, flat {flat}"
+
+
+def positive(n, d, dtype, shape, seed, dead=0):
+    """Queries, keys and a V of positive elements on the device, and the definition's results in
+    float64.  shape "even": logits of order 1; "rising", "falling": by 40 along the keys; the
+    first `dead` keys have logits of -inf."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = torch.randn(4, d, device=DEV, generator=g)
+    k = torch.randn(n, d, device=DEV, generator=g)
+    v = (torch.rand(n, d, device=DEV, generator=g) + 0.5).to(dtype)
+    q[:, 0] = 1.0
+    k[:, 0] = torch.linspace(-20, 20, n, device=DEV) * {"even": 0, "rising": 1, "falling": -1}[shape] * math.sqrt(d)
+    q, k = q.to(dtype), k.to(dtype)
+    k[:dead, 0] = -math.inf
+    return q, k, v
+
+
+def long_reference(q, k, v):
+    scale = float(torch.tensor(1 / math.sqrt(q.shape[1]), dtype=torch.float32))
+    x = (q.double() @ k.double().T) * scale
+    z = torch.logsumexp(x, -1)
+    mag = float((q.abs().double() @ k.nan_to_num(neginf=0.0).abs().double().T).max()) * scale
+    return torch.exp(x - z[:, None]) @ v.double(), z, mag
+
+
+def hold_long(out, lse, ref, dtype, weight_type, drained, n, what):
+    """The sums of positive terms.  The tensor cores cut what they add: each of 16 products by
+    less than 2^-25 of the sum so far and the sum by less than 2^-23 of it, over `drained` keys;
+    what they have summed is then added in float32 (half a unit of 2^-23 each time)."""
+    o, z, mag = ref
+    cut = drained / 16 * (2.0 ** -21 + 2.0 ** -23) + (n / drained + 8) * 2.0 ** -24
+    rel = half(weight_type) + 4.2 * 160 * 2.0 ** -24 * (mag + 1) + cut + half(dtype)
+    off = ((out.double() - o) / o).abs().max().item()
+    assert off <= rel * (1 + 2.0 ** -8), f"{what}: off by {off}, {off / rel} of the bound"
+    assert float((lse.double() - z).abs().max()) <= 4.2 * 160 * 2.0 ** -24 * (mag + 1) + 2.0 ** -14, what
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tiles", [1, 2])
+@pytest.mark.parametrize("dtype,d,n,shape,dead", [
+    ("f16", 64, 2 ** 20, "even", 0), ("f16", 128, 2 ** 20 - 77, "even", 0), ("bf16", 64, 2 ** 22, "even", 0),
+    ("bf16", 128, 300000, "rising", 0), ("f16", 64, 300001, "falling", 0), ("f16", 128, 200000, "even", 50000),
+    ("bf16", 64, 16384 + 1, "even", 0), ("f16", 128, 2 * 16384, "even", 0)])
+def test_prompt_sums_over_long_sequences(dtype, d, n, shape, dead, tiles):
+    """A query behind up to 2^22 keys, in items of one and (among many empty sequences) two tiles."""
+    q, k, v = positive(n, d, TYPES[dtype], shape, 61, dead)
+    ref = long_reference(q, k, v)
+    batch = 1 if tiles == 1 else 200
+    cu_q, cu_k = (torch.tensor([0] * (batch // 2) + [m] * (batch - batch // 2 + 1), dtype=torch.int32, device=DEV)
+                  for m in (1, n))
+    cu_q[0] = cu_k[0] = 0
+    ws = hs2.packed_workspace(DEV)
+    out, lse = hs2.packed_attn(q[None], k[:, None], v[:, None], cu_q, cu_k, ws)
+    assert hs2.check_device_status(ws) == 0
+    hold_long(out[0], lse[0], ref, TYPES[dtype], TYPES[dtype], 16384, n, f"{shape}, {tiles} tiles")
