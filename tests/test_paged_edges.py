@@ -7,7 +7,7 @@ import torch
 
 from long_context_token_b200 import hs2
 
-from _paged_ref import Pool, TYPES, attend, check
+from _paged_ref import Pool, TYPES, attend, check, quantise
 from test_paged import DEV, L, P, _kv, cache_of, cu_of, same  # noqa: F401 (L is a fixture)
 
 
@@ -338,3 +338,41 @@ def test_prompt_sums_over_long_sequences(dtype, d, n, shape, dead, tiles):
     out, lse = hs2.packed_attn(q[None], k[:, None], v[:, None], cu_q, cu_k, ws)
     assert hs2.check_device_status(ws) == 0
     hold_long(out[0], lse[0], ref, TYPES[dtype], TYPES[dtype], 16384, n, f"{shape}, {tiles} tiles")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,d,group,n,shape,dead", [
+    ("f16", 64, 128, 2 ** 20, "even", 0), ("fp8", 64, 100, 2 ** 20, "even", 0), ("bf16", 128, 40, 2 ** 19, "rising", 0),
+    ("f16", 128, 20, 2 ** 18, "falling", 0), ("f16", 64, 4, 2 ** 20, "even", 0), ("f16", 64, 12, 2 ** 19, "even", 0),
+    ("f16", 64, 128, 100000, "even", 30000)])
+def test_step_sums_over_long_sequences(kv, d, group, n, shape, dead):
+    """160 sequences on the same pages, so that a CTA takes about a whole one."""
+    dt, batch, page = (torch.bfloat16 if kv == "bf16" else torch.float16), 160, 64
+    q, k, v = positive(n, d, dt, shape, 62, dead)
+    num = -(-n // page)
+    shape4 = (num, 1, page, d)
+    scales = ()
+    if kv == "fp8":
+        kc, ks = quantise(k.cpu())
+        vc, vs = quantise(v.cpu())
+        pools = [torch.zeros(shape4, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        scales = [torch.zeros(shape4[:3], device=DEV) for _ in range(2)]
+        for p, s, c, x in zip(pools, scales, (kc, vc), (ks, vs)):
+            p.view(-1, d)[:n], s.view(-1)[:n] = c.to(DEV), x.to(DEV)
+        k, v = ((c.view(torch.float8_e4m3fn).double() * x.double()[:, None]).to(DEV) for c, x in ((kc, ks), (vc, vs)))
+    else:
+        pools = [torch.zeros(shape4, dtype=dt, device=DEV) for _ in range(2)]
+        for p, x in zip(pools, (k, v)):
+            p.view(-1, d)[:n] = x
+    ref = long_reference(q, k, v)
+    pages = torch.arange(num, dtype=torch.int32, device=DEV).repeat(batch, 1)
+    lens = torch.full((batch,), n, dtype=torch.int32, device=DEV)
+    cache = hs2.PagedCache(*pools, pages, lens, *scales)
+    ws = hs2.paged_workspace(cache, group)
+    heads = q.repeat(group // 4, 1)[None].repeat(batch, 1, 1)
+    out, lse = hs2.paged_attn(heads, cache, ws)
+    assert hs2.check_device_status(ws) == 0
+    for b in (0, 1, batch // 2, batch - 1):
+        for h in range(0, group, 4):
+            hold_long(out[b, h:h + 4], lse[b, h:h + 4], ref, dt, torch.float16 if kv == "fp8" else dt, 16384, n,
+                      f"{shape}, sequence {b}, head {h}")
