@@ -413,7 +413,8 @@ HS2_API size_t hs2_packed_workspace_bytes(void);
  * Logits that are NaN or +inf make the results of the queries that see their keys NaN; a
  * query whose visible logits are all -inf gives 0 and -inf.  A non-finite V row may reach
  * every query of its own sequence, and no other; padding rows reach none.
- * cu entries that descend or pass n_q / n_k set HS2_ERR_BAD_LENGTH and are clamped.  n_q 0
+ * cu entries that descend or pass n_q / n_k, and a sequence of more than 2^26 keys, set
+ * HS2_ERR_BAD_LENGTH and are clamped (the sequence to its first 2^26 keys).  n_q 0
  * does nothing; n_q < (2^31 - 4096) / h_q, n_k < (2^31 - 4096) / n_kv_heads; batch <= 65535. */
 HS2_API hs2_status hs2_packed_attn(const hs2_packed* p, float sm_scale, void* out, float* lse,
                                    void* workspace, size_t ws_bytes, hs2_stream_t stream);

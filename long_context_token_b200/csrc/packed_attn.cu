@@ -50,6 +50,9 @@ constexpr int kKeys = 128;         // keys per loaded block
 constexpr int kStep = 64;          // keys per step (the MMA's N, then its K extent)
 constexpr int kSoftmaxThreads = 256;
 constexpr int kPackedThreads = kSoftmaxThreads + 128;
+// Keys of a sequence: warps that wait for an item's end (the cleaner, and tile 1's softmax in
+// items of one tile) would give up after mbar_wait's limit, about 150 million keys.
+constexpr int kMaxKeys = 1 << 26;
 constexpr int kOneTileUpTo = 1;    // see launch_packed
 constexpr int kDrainSteps = 256;   // steps between which O leaves the tensor cores' sum
 constexpr float kMoveAt = 8.0f;    // log2 units by which a logit may pass the reference
@@ -187,6 +190,10 @@ struct ItemCursor {
       k0 = min(max(c, 0), p.n_k);
       lq = max(min(b, p.n_q) - q0, 0);
       lk = max(min(d, p.n_k) - k0, 0);
+      if (lk > kMaxKeys) {
+        set_status(p.status, HS2_ERR_BAD_LENGTH);
+        lk = kMaxKeys;
+      }
     }
     blocks = (lq + tokens_per_item - 1) / tokens_per_item;
     total = __reduce_add_sync(0xffffffffu, (uint32_t)blocks) * (uint32_t)p.h_kv;

@@ -376,3 +376,21 @@ def test_step_sums_over_long_sequences(kv, d, group, n, shape, dead):
         for h in range(0, group, 4):
             hold_long(out[b, h:h + 4], lse[b, h:h + 4], ref, dt, torch.float16 if kv == "fp8" else dt, 16384, n,
                       f"{shape}, sequence {b}, head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [1, 200])  # one and two tiles per work item
+def test_a_sequence_that_one_block_walks_for_a_second(batch):
+    """2^26 keys, the most of a sequence (rows 16 bytes apart, so that they fit): no wait gives
+    up.  Equal logits and a V of ones: sums of 16384 keys are exact, and so are their sums.  Four
+    times as many are refused; the first 2^26 still give the same."""
+    n, d = 2 ** 28, 64
+    k = torch.zeros(8 * n + d, dtype=torch.bfloat16, device=DEV).as_strided((n, 1, d), (8, d, 1))
+    v = torch.ones(8 * n + d, dtype=torch.bfloat16, device=DEV).as_strided((n, 1, d), (8, d, 1))
+    q = torch.randn(1, 1, d, device=DEV).to(torch.bfloat16)
+    ws = hs2.packed_workspace(DEV)
+    for m, code in ((2 ** 26, 0), (n, 7)):
+        cu_q, cu_k = (torch.tensor([0] + [x] * batch, dtype=torch.int32, device=DEV) for x in (1, m))
+        out, lse = hs2.packed_attn(q, k, v, cu_q, cu_k, ws)
+        assert hs2.check_device_status(ws) == code
+        assert bool((out == 1).all()) and abs(lse.item() - math.log(2 ** 26)) < 1e-4
