@@ -442,6 +442,8 @@ HS2_API void hs2_set_deterministic(int on);
 /* Test hook for the error path of the bounded device-side waits; not for production.
  *   mode 1: the bf16 one-token full-layer kernel issues no loads and no MMAs, so its
  *           softmax warps' first wait on an MMA result runs out (after about 10 us);
+ *           hs2_paged_attn and hs2_packed_attn issue no loads, so the first waits of
+ *           their other warps run out (after the normal limit, about two seconds);
  *   mode 2: the fused selection tail's row barriers wait for one CTA more than the row
  *           has, so each runs out (after about 10 us);
  *   mode 0: normal operation (the default).

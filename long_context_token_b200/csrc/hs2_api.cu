@@ -24,8 +24,9 @@ constexpr int kTargetCtas = 4 * 148;
 constexpr int kMinChunk = 256;
 constexpr int kChunk4 = 64;
 
-// The bounded-wait test hook (hs2_debug_stall_waits): copied into every full-layer launch.
-static int g_stall_test = 0;
+// The bounded-wait test hook (hs2_debug_stall_waits): copied into every full-layer launch (and,
+// in paged_api.cu, into those of the paged and packed attention).
+int g_stall_test = 0;
 // hs2_set_deterministic: static key chunks in the full layer (no run-time tile sharing).
 static int g_deterministic = 0;
 

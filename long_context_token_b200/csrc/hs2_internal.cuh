@@ -60,6 +60,8 @@ struct WsLayout {
 // Records a CUDA error's text for hs2_last_cuda_error; returns HS2_ERR_CUDA.
 hs2_status cuda_fail(cudaError_t e, const char* what);
 
+extern int g_stall_test;  // hs2_debug_stall_waits
+
 int plan_splits1(int bq, int max_len, int num_sms);
 int device_sm_count();
 int plan_splits4(int idx_width);

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       }
       if (!it.valid) break;
       const int blocks = (max(it.n[0], it.n[1]) * kStep + kKeys - 1) / kKeys;
-      if (lane == 0 && blocks > 0) {
+      if (lane == 0 && blocks > 0 && !p.stall_test) {
         auto fill = [&](const CUtensorMap* m, int x, int y, int z, int boxes) {
           const uint32_t s = slot % NS;
           wait(empty + s, ((slot / NS) & 1) ^ 1);

@@ -57,6 +57,7 @@ struct PagedAttnParams {
   float* lse;
   uint32_t* counters;
   float* partials;
+  int stall_test;  // hs2_debug_stall_waits: the producers issue no loads
 };
 
 // Workspace of hs2_packed_attn: the status word, then at kPackedSyncOff the next work item
@@ -77,6 +78,7 @@ struct PackedAttnParams {
   float* lse;
   uint32_t* status;
   uint32_t* sync;
+  int stall_test;  // hs2_debug_stall_waits: no loads are issued
 };
 
 cudaError_t launch_paged_write(const PagedMoveParams& p, int head_dim, int cache_dtype,

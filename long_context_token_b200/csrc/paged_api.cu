@@ -180,6 +180,7 @@ hs2_status hs2_paged_attn(const void* q, int dtype, int h_q, int64_t q_seq_strid
   p.lse = lse;
   p.counters = ws_ptr<uint32_t>(workspace, kPagedCounterOff);
   p.partials = ws_ptr<float>(workspace, kPagedPartialOff);
+  p.stall_test = g_stall_test == 1;
   const cudaError_t e = launch_paged_attn(p, kv->head_dim, kv->dtype, dtype, stream);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e, "paged attention launch");
 }
@@ -230,6 +231,7 @@ hs2_status hs2_packed_attn(const hs2_packed* a, float sm_scale, void* out, float
   p.lse = lse;
   p.status = static_cast<uint32_t*>(workspace);
   p.sync = ws_ptr<uint32_t>(workspace, kPackedSyncOff);
+  p.stall_test = g_stall_test == 1;
   const cudaError_t e = launch_packed_attn(p, a->head_dim, a->dtype, stream);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e, "packed attention launch");
 }

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     const uint32_t box_bytes = (uint32_t)rows * RB;
     uint32_t slot = 0;  // this run's tiles so far
     uint32_t mine = 0;  // of them, this warp's last one + 1 (0: none)
-    while (ok && walk.next(p, s)) {
+    while (ok && !p.stall_test && walk.next(p, s)) {
       const int32_t* table = p.c.pages + (size_t)s.b * p.c.max_pages;
       const int last_page = (s.len - 1) >> shift;
       auto load_pages = [&](int from) {

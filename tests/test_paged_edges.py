@@ -1,6 +1,8 @@
 """Paged caches and packed prompts at the edges of what their definitions allow."""
 import ctypes
+import functools
 import math
+import time
 
 import pytest
 import torch
@@ -8,7 +10,7 @@ import torch
 from long_context_token_b200 import hs2
 
 from _paged_ref import Pool, TYPES, attend, check, quantise
-from test_paged import DEV, L, P, _kv, cache_of, cu_of, same  # noqa: F401 (L is a fixture)
+from test_paged import DEV, L, P, _kv, cache_of, check_prompts, check_step, cu_of, same  # noqa: F401 (L is a fixture)
 
 
 # ---------------------------------------------------------------- the host's checks (CPU)
@@ -394,3 +396,43 @@ def test_a_sequence_that_one_block_walks_for_a_second(batch):
         out, lse = hs2.packed_attn(q, k, v, cu_q, cu_k, ws)
         assert hs2.check_device_status(ws) == code
         assert bool((out == 1).all()) and abs(lse.item() - math.log(2 ** 26)) < 1e-4
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_are_reported_and_end():
+    """With no loads issued, every warp that waits for one gives up once and the kernels wind
+    down: partial results and counters too, so that the calls after them need only a clean
+    status.  (Prompts in items of one and of two tiles, a step in parts and in groups of them.)"""
+    lib = hs2.lib()
+    step = Pool([40000, 300, 0], 1, 128, 32, "bf16", seed=63)
+    q = torch.randn(3, 16, 128, generator=torch.Generator().manual_seed(64)).to(torch.bfloat16)
+    cache = cache_of(step)
+    ws, pws = hs2.paged_workspace(cache, 16), hs2.packed_workspace(DEV)
+    prompts = []
+    for heads, lens in (((4, 2), [300, 1]), ((40, 40), [300, 70, 0, 129])):
+        x = torch.randn(sum(lens), heads[0] + 2 * heads[1], 64, generator=torch.Generator().manual_seed(65)).half()
+        prompts.append((x[:, :heads[0]], x[:, heads[0]:sum(heads)], x[:, sum(heads):], lens))
+
+    def prompt(a, k, v, lens):
+        return hs2.packed_attn(a.to(DEV), k.to(DEV), v.to(DEV), cu_of(lens).to(DEV), workspace=pws)
+
+    calls = [(ws, lambda: hs2.paged_attn(q.to(DEV), cache, ws))] + \
+        [(pws, functools.partial(prompt, *p)) for p in prompts]
+    for w, call in calls:
+        lib.hs2_debug_stall_waits(1)
+        try:
+            begin = time.monotonic()
+            call()
+            torch.cuda.synchronize()
+            took = time.monotonic() - begin
+        finally:
+            lib.hs2_debug_stall_waits(0)
+        assert hs2.check_device_status(w) == 5
+        assert took < 12, f"{took} s to give up"
+        assert hs2.check_device_status(w) == 0
+        w.zero_()
+    check_step(step, q, *calls[0][1]())
+    for (a, k, v, lens), (w, call) in zip(prompts, calls[1:]):
+        out, lse = call()
+        check_prompts(a, k, v, lens, lens, out, lse)
+    assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
