@@ -39,6 +39,8 @@
 // sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 95 us, 5.3 TB/s, 0.81.  Groups of 64
 // and more heads are bound by the products and conversions, which every 16 heads repeat: one
 // sequence of 1048576 FP8 keys under 64 heads takes 190 us, 4.5 times its bytes' time.
+#include <atomic>
+
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tc_common.cuh"
@@ -957,13 +959,15 @@ static cudaError_t launch_paged_k(const PagedAttnParams& p, unsigned grid, cudaS
   auto* kernel = paged_attn_kernel<D, Q, kFp8, NT, kDrain>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  static bool checked = false;  // (a race only checks twice)
-  if (!checked) {
+  // With fewer registers at launch the consumers would wait for more for good.  (The tests hold
+  // the build to the number; this is for builds that nobody tested.)
+  static std::atomic<bool> checked{false};  // (two threads may both check)
+  if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
     const cudaError_t q = cudaFuncGetAttributes(&a, kernel);
     if (q != cudaSuccess) return q;
     if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    checked = true;
+    checked.store(true, std::memory_order_relaxed);
   }
   return launch_pdl(kernel, dim3(grid), dim3(kPagedThreads), L::kBytes, st, tk, tv, p);
 }

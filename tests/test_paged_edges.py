@@ -2,12 +2,15 @@
 import ctypes
 import functools
 import math
+import os
+import re
+import subprocess
 import time
 
 import pytest
 import torch
 
-from long_context_token_b200 import hs2
+from long_context_token_b200 import build, hs2
 
 from _paged_ref import Pool, TYPES, attend, check, quantise
 from test_paged import DEV, L, P, _kv, cache_of, check_prompts, check_step, cu_of, same  # noqa: F401 (L is a fixture)
@@ -21,6 +24,21 @@ def test_scales_that_float32_cannot_hold_in_log2_units_are_refused(L, scale, cod
     assert L.hs2_paged_attn(P, 0, 16, 2048, 128, ctypes.byref(kv), scale, P, P, P, 16, None) == code
     p = hs2.Packed(P, P, P, P, P, 1024, 128, 256, 128, 10, 20, 2, 8, 2, 128, 0)
     assert L.hs2_packed_attn(ctypes.byref(p), scale, P, P, P, 16, None) == code
+
+
+def test_step_kernels_are_built_with_the_registers_that_they_share_out(tmp_path):
+    """Their warps take and give back registers of those that the block was launched with."""
+    source = os.path.join(build.CSRC, "paged_attn.cu")
+    text = open(source).read()
+    launch, consumers, producers = map(int, re.search(
+        r"kLaunchRegs = (\d+), kConsumerRegs = (\d+), kProducerRegs = (\d+);", text).groups())
+    assert 256 * consumers + 128 * producers <= 384 * launch
+    flags = [f for f in build.NVCC_FLAGS if f not in ("-lineinfo", "--threads", "0")]
+    out = subprocess.run([build.nvcc(), *flags, "-I", os.path.join(build.ROOT, "include"), "-Xptxas", "-v",
+                          "-cubin", "-o", str(tmp_path / "step.cubin"), source], capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    used = re.findall(r"Compiling entry function '\w*paged_attn_kernel\w*'.*?Used (\d+) registers", out.stderr, re.S)
+    assert len(used) == 32 and set(map(int, used)) == {launch}
 
 
 # ---------------------------------------------------------------- on the GPU
