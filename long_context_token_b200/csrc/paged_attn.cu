@@ -10,7 +10,7 @@
 //                  entries ahead), one TMA load per page and tensor into a ring of 128 KB,
 //                  float32 scales of an FP8 cache by 4-byte asynchronous copies.  (One warp
 //                  spends about 600 cycles on a tile, 1200 with scales: too slow alone.)
-//   8 warps        flash decoding with mma.sync m16n8k16, transposed: S^T = K Q^T with 16
+//   8 warps        attention with mma.sync m16n8k16, transposed: S^T = K Q^T with 16
 //                  keys as the rows and 8 heads as the columns, O^T += V^T P^T, so a group
 //                  of 7 or 8 heads wastes nothing and P goes from accumulator to operand
 //                  by a transposing move within the warp.  The tensor work is a few per
@@ -23,7 +23,9 @@
 // The softmax reference moves only when a logit passes it by more than 8 (log2 units), so a
 // tile has no shuffles.  A weight is rounded once, to the type of the second product: bfloat16,
 // or float16 scaled so that the largest lies in [2^7, 2^15], half a step each down to 2^-21 of
-// it and 2^-32 of it below.  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
+// it and 2^-32 of it below.  (A second bfloat16 term for each weight, as the contiguous layers
+// keep, brings results from 0.0024 of their size to 0.0017, their own rounding, and costs 3 % of
+// the time with 16 heads per K/V head, 8 % with 128; it is left out.)  An FP8 row's scale is folded into its weight: w = 2^(x - m) * s_v,
 // with m following max(x + log2 s_v) over the rows of V that are not all zeros, so w is rounded
 // to float16 relative to the largest weight however the scales vary; E4M3 codes are exact in float16.  A bfloat16
 // query against codes is brought to float16 by a power of two per head, exactly down to
@@ -35,10 +37,11 @@
 // What bounds it: memory while the runs last (7 TB/s of rows in the steady state), and 6 to
 // 10 us of latencies around them: the run and the first pages (3 us), the join within the CTA,
 // the arrival and the join of the parts (4 us).  On a B200, 8 x 131072 bfloat16 keys of one
-// K/V head under 16 query heads: 90 us, 5.94 TB/s, 0.91 of the measured copy rate; 64
-// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 95 us, 5.3 TB/s, 0.81.  Groups of 64
+// K/V head under 16 query heads: 91 us, 5.9 TB/s, 0.90 of the measured copy rate; 64
+// sequences of 1 .. 8191 FP8 keys, 8 K/V heads under 64: 96 us, 5.2 TB/s, 0.80.  Groups of 32
 // and more heads are bound by the products and conversions, which every 16 heads repeat: one
-// sequence of 1048576 FP8 keys under 64 heads takes 190 us, 4.5 times its bytes' time.
+// sequence of 1048576 FP8 keys under 64 heads takes 188 us, 4.5 times its bytes' time, one of
+// 131072 57 us (11 times), 64 of 8192 under 128 heads 178 us (8 times).
 #include <atomic>
 
 #include "paged.cuh"
@@ -61,7 +64,9 @@ constexpr int kPagedThreads = kConsumers + 32 * kProducerWarps;
 constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
 constexpr int kJoinAtOnce = 512;  // rows (heads x partial results) that one CTA joins alone
 constexpr int kDrainTiles = 512;  // tiles that a warp adds up before its outputs leave the registers
-constexpr int kMinTiles = 8;  // a run is at least a tile for each warp
+// A run is at least a tile for each warp.  (4096 bfloat16 keys, 16 heads on one: 12.6 us with 8,
+// 13.7 with 4, 12.9 with 16; 16384 keys: 15.1, 16.1, 16.8; 1024 keys: 11.3, 10.3, 12.8.)
+constexpr int kMinTiles = 8;
 constexpr float kMoveAt = 8.0f;
 constexpr float kNoScale = -64.f;  // log2 that stands for a V scale of 0 (and any below 2^-64)
 constexpr float kLn2 = 0.69314718055994531f;
