@@ -28,7 +28,13 @@
 // repeats until the power cap lowers the clock (0.80 of the measured sustained rate).  What
 // was measured on the way to this shape, on that prompt: 128-key steps with one S buffer per
 // tile 1040 us; the MMAs of both tiles from one warp 942; without taking turns 878; two
-// threads per row 904.
+// threads per row 904.  At d 64 the exponentials and the step's fixed costs are the same for half
+// the products: one prompt of 16384 tokens 760 us, 2.3 times its floor.
+//
+// Keys are never split: an item walks all keys that its rows see on one SM.  Few queries after a
+// long prefix leave the other SMs idle: 64 tokens of 16 heads (one K/V head) at the end of 131072
+// keys take 1380 us, 33 times their floor; 512 tokens at the end of 16000 (two K/V heads) 168, 4.2
+// times.
 //
 // Weights are rounded to the inputs' 16-bit type for the second product, as the MMA needs
 // (float16 ones scaled so that the largest lies in [2^7, 2^15]); the row sums, references and O
@@ -105,7 +111,8 @@ __host__ __device__ constexpr uint64_t v_step(int kk) { return (uint64_t)(kk * 1
 // (2.6e-6, from the Remez exchange), times 2^n.  Of each kPairsOf pairs of
 // weights kPairsByFma are formed this way, to relieve the special-function units: one in
 // eight (none 862 us on the prompt above, one 841, two 855, three 865, four 887: the
-// multiply-add pipes and the issue slots are not free either).
+// multiply-add pipes and the issue slots are not free either; 8192 tokens at d 64, 16 heads on 2:
+// none 210, one 205, two 207).
 constexpr int kPairsOf = 8, kPairsByFma = 1;
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   // (Below -126.5 the factor 2^n is 0, so a masked key weighs nothing; a NaN stays one.)
