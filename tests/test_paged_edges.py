@@ -454,3 +454,33 @@ def test_waits_that_run_out_are_reported_and_end():
         out, lse = call()
         check_prompts(a, k, v, lens, lens, out, lse)
     assert hs2.check_device_status(ws) == 0 and hs2.check_device_status(pws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,h_q,h_kv", [("f16", 64, 2, 1), ("bf16", 128, 6, 2), ("f16", 128, 7, 7)])
+def test_prompts_longer_than_one_sum(dtype, d, h_q, h_kv):
+    """Whole prompts of more keys than are summed at once: the queries around the first ones that
+    see 16384 and 32768 keys, whose two tiles leave the sum at different steps, and the last."""
+    lens = [33000, 16385, 300]
+    t, dt = sum(lens), TYPES[dtype]
+    g = torch.Generator(device=DEV).manual_seed(66)
+    q, k = (torch.randn(t, h, d, device=DEV, generator=g).to(dt) for h in (h_q, h_kv))
+    v = (torch.rand(t, h_kv, d, device=DEV, generator=g) + 0.5).to(dt)
+    ws = hs2.packed_workspace(DEV)
+    out, lse = hs2.packed_attn(q, k, v, cu_of(lens).to(DEV), workspace=ws)
+    assert hs2.check_device_status(ws) == 0
+    scale = float(torch.tensor(1 / math.sqrt(d), dtype=torch.float32))
+    at = 0
+    for n in lens:
+        for lo in (0, 16200, 16384, 32700, n - 130):
+            hi = min(lo + 140, n)
+            if lo >= hi or lo < 0:
+                continue
+            rows, seen = slice(at + lo, at + hi), torch.arange(lo, hi, device=DEV)[:, None]
+            for h in range(h_q):
+                qq, kk, vv = q[rows, h].double(), k[at:at + hi, h * h_kv // h_q].double(), v[at:at + hi, h * h_kv // h_q].double()
+                x = torch.where(torch.arange(hi, device=DEV) <= seen, (qq @ kk.T) * scale, -math.inf)
+                z = torch.logsumexp(x, -1)
+                ref = torch.exp(x - z[:, None]) @ vv, z, float((qq.abs() @ kk.abs().T).max()) * scale
+                hold_long(out[rows, h], lse[rows, h], ref, dt, dt, 16384, n, f"prompt of {n}, from {lo}, head {h}")
+        at += n
